@@ -17,9 +17,15 @@ Entry points (same names as the C ABI):
     qlora_linear_fwd(X, w, A, B, s)              -> (Y, T)
     qlora_linear_bwd(dY, X, w, A, B, s, T=None)  -> (dX, dA, dB)
     qlora_fp8_e4m3_encode(x)                     -> uint8 tensor
+    qlora_int8_quantize_rows(x)                  -> Int8Rows
+    qlora_int8_linear_fwd(X, w)                  -> Y
+    qlora_int8_linear_bwd(dY, w)                 -> dX
+    qlora_int8_expert_fwd(X, w, offsets)         -> Y
+    qlora_int8_expert_bwd(dY, w, offsets)        -> dX
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -75,6 +81,17 @@ def _load() -> ctypes.CDLL:
         "qlora_debug_wait_timeout": (i32, [ctypes.c_uint64, vp]),
         "qlora_int8_quantize": (i32, [vp, i64, i32, vp, vp, vp, vp]),
         "qlora_int8_dequantize": (i32, [vp, vp, i64, i32, vp, vp]),
+        "qlora_int8_quantize_rows": (i32, [vp, i32, i64, i64, vp, vp, vp, vp]),
+        "qlora_int8_linear_fwd_workspace_size": (sz, [i64, i64, i64]),
+        "qlora_int8_linear_bwd_workspace_size": (sz, [i64, i64, i64]),
+        "qlora_int8_linear_fwd": (i32, [vp, i64, i64, i64, vp, vp, vp, i32, vp, sz, vp]),
+        "qlora_int8_matmul": (i32, [vp, vp, i64, i64, i64, vp, vp, vp, i32, vp, sz, vp]),
+        "qlora_int8_linear_bwd": (i32, [vp, i64, i64, i64, vp, vp, vp, vp, sz, vp]),
+        "qlora_int8_expert_fwd_workspace_size": (sz, [i64, i32, i64, i64]),
+        "qlora_int8_expert_bwd_workspace_size": (sz, [i64, i32, i64, i64]),
+        "qlora_int8_expert_fwd": (i32, [vp, vp, i64, i32, i64, i64, vp, vp, vp, i32, vp, sz, vp]),
+        "qlora_int8_expert_matmul": (i32, [vp, vp, vp, i64, i32, i64, i64, vp, vp, vp, i32, vp, sz, vp]),
+        "qlora_int8_expert_bwd": (i32, [vp, vp, i64, i32, i64, i64, vp, vp, vp, vp, sz, vp]),
         "qlora_debug_fill": (i32, [vp, i64, ctypes.c_uint32, vp]),
         "qlora_debug_read": (i32, [vp, i64, ctypes.c_uint32, vp, vp]),
         "qlora_linear_group_fwd_workspace_size": (sz, [i64, i32, i32]),
@@ -527,6 +544,188 @@ def qlora_int8_dequantize(codes, c, block: int = 64, out=None, stream=None):
     _check("qlora_int8_dequantize", _get_lib().qlora_int8_dequantize(_ptr(codes), _ptr(c), n, int(block),
                                                                      _ptr(out), _stream(stream)))
     return out
+
+
+# ------------------------------------------------ Int8 linear, dense and by expert
+
+@dataclass
+class Int8Rows:
+    """Rows of Int8 codes with one fp32 scale each: tokens (M x K), a frozen
+    weight (N x K, a scale per output channel) or the weights of E experts
+    (E x N x K).  Rows of codes are padded with zeros to 16 bytes."""
+    codes: object  # int8 [..., round_up(K, 16)]
+    scale: object  # float32 [...]
+    shape: tuple   # (..., K)
+
+    def nbytes(self) -> int:
+        return sum(int(t.numel() * t.element_size()) for t in (self.codes, self.scale))
+
+
+def _alloc_on(stream):
+    """Buffers made inside belong to `stream` (None: the current one), so that
+    torch's allocator hands their memory on only in that stream's order."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
+def alloc_int8_rows(shape, device) -> Int8Rows:
+    torch = _torch()
+    shape = tuple(int(d) for d in shape)
+    return Int8Rows(torch.empty(shape[:-1] + (-(-shape[-1] // 16) * 16,), dtype=torch.int8, device=device),
+                    torch.empty(shape[:-1], dtype=torch.float32, device=device), shape)
+
+
+def _need_int8_rows(name, r, dims):
+    """Codes and scales of an Int8Rows hold exactly what its shape says."""
+    torch = _torch()
+    if len(r.shape) != dims:
+        raise ValueError(f"{name} must be {dims}-D, got shape {tuple(r.shape)}")
+    lead, K = tuple(int(d) for d in r.shape[:-1]), int(r.shape[-1])
+    _need_shape(f"{name}.codes", r.codes, lead + (-(-K // 16) * 16,))
+    _need_shape(f"{name}.scale", r.scale, lead)
+    _need_dtype(torch.int8, **{f"{name}.codes": r.codes})
+    _need_dtype(torch.float32, **{f"{name}.scale": r.scale})
+
+
+def qlora_int8_quantize_rows(x, out: Int8Rows | None = None, status=None, stream=None) -> Int8Rows:
+    """Int8 absmax quantization of the rows (the last dimension) of a bf16 or
+    fp32 CUDA tensor, one scale per row: tokens, or a weight by output channel."""
+    torch = _torch()
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"x must be float32 or bfloat16, got {x.dtype}")
+    if x.dim() < 2 or int(x.shape[-1]) < 1:
+        raise ValueError("x must have at least two dimensions and a non-empty last one")
+    with _alloc_on(stream):
+        r = out if out is not None else alloc_int8_rows(x.shape, x.device)
+    if tuple(r.shape) != tuple(x.shape):
+        raise ValueError(f"out has shape {tuple(r.shape)}, x {tuple(x.shape)}")
+    _need_int8_rows("out", r, x.dim())
+    if status is not None:
+        _need_dtype(torch.int32, status=status)
+    _need_cuda(x, r.codes, r.scale, status)
+    K = int(x.shape[-1])
+    _check("qlora_int8_quantize_rows",
+           _get_lib().qlora_int8_quantize_rows(_ptr(x), 0 if x.dtype == torch.float32 else 1, x.numel() // K, K,
+                                               _ptr(r.codes), _ptr(r.scale), _ptr(status), _stream(stream)))
+    return r
+
+
+def qlora_int8_linear_fwd_workspace_size(M, N, K) -> int:
+    return int(_get_lib().qlora_int8_linear_fwd_workspace_size(int(M), int(N), int(K)))
+
+
+def qlora_int8_linear_bwd_workspace_size(M, N, K) -> int:
+    return int(_get_lib().qlora_int8_linear_bwd_workspace_size(int(M), int(N), int(K)))
+
+
+def qlora_int8_expert_fwd_workspace_size(T, E, N, K) -> int:
+    return int(_get_lib().qlora_int8_expert_fwd_workspace_size(int(T), int(E), int(N), int(K)))
+
+
+def qlora_int8_expert_bwd_workspace_size(T, E, N, K) -> int:
+    return int(_get_lib().qlora_int8_expert_bwd_workspace_size(int(T), int(E), int(N), int(K)))
+
+
+def _int8_dims(rows, w, offsets, backward):
+    """(T, E, N, K) of an Int8 call; offsets None: the dense linear, E = 1."""
+    torch = _torch()
+    _need_int8_rows("w", w, 2 if offsets is None else 3)
+    E = 1 if offsets is None else int(w.shape[0])
+    N, K = (int(d) for d in w.shape[-2:])
+    name, width = ("dY", N) if backward else ("X", K)
+    if isinstance(rows, Int8Rows):
+        if backward:
+            raise ValueError("dY must be a bfloat16 tensor")
+        _need_int8_rows(name, rows, 2)
+    else:
+        if rows.dim() != 2:
+            raise ValueError(f"{name} must be 2-D")
+        _need_dtype(torch.bfloat16, **{name: rows})
+    if int(rows.shape[1]) != width:
+        raise ValueError(f"{name} has {rows.shape[1]} columns but the weight is {N} x {K}")
+    if offsets is not None:
+        _need_shape("offsets", offsets, (E + 1,))
+        _need_dtype(torch.int32, offsets=offsets)
+    return int(rows.shape[0]), E, N, K
+
+
+def _int8_fwd(X, w, offsets, out_dtype, Y, ws, stream):
+    torch = _torch()
+    T, E, N, K = _int8_dims(X, w, offsets, False)
+    quantized = isinstance(X, Int8Rows)
+    if Y is not None and out_dtype is None:
+        out_dtype = Y.dtype
+    out_dtype = out_dtype or torch.bfloat16
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
+    _need_shape("Y", Y, (T, N))
+    _need_dtype(out_dtype, Y=Y)
+    x_bufs = (X.codes, X.scale) if quantized else (X,)
+    _need_cuda(*x_bufs, w.codes, w.scale, offsets, Y, ws)
+    by_expert = offsets is not None
+    with _alloc_on(stream):
+        if Y is None:
+            Y = torch.empty((T, N), dtype=out_dtype, device=w.codes.device)
+        if ws is None:
+            need = (qlora_int8_expert_fwd_workspace_size(T, E, N, K) if by_expert
+                    else qlora_int8_linear_fwd_workspace_size(T, N, K))
+            ws = _workspace(need, w.codes.device)
+    fn = ("qlora_int8_expert_" if by_expert else "qlora_int8_") + \
+        ("matmul" if quantized else "fwd" if by_expert else "linear_fwd")
+    sizes = (_ptr(offsets), T, E, N, K) if by_expert else (T, N, K)
+    st = getattr(_get_lib(), fn)(*(_ptr(t) for t in x_bufs), *sizes, _ptr(w.codes), _ptr(w.scale), _ptr(Y),
+                                 0 if out_dtype == torch.float32 else 1, _ptr(ws), ws.numel(), _stream(stream))
+    _check(fn, st)
+    return Y
+
+
+def _int8_bwd(dY, w, offsets, dX, ws, stream):
+    torch = _torch()
+    T, E, N, K = _int8_dims(dY, w, offsets, True)
+    _need_shape("dX", dX, (T, K))
+    _need_dtype(torch.bfloat16, dX=dX)
+    _need_cuda(dY, w.codes, w.scale, offsets, dX, ws)
+    by_expert = offsets is not None
+    with _alloc_on(stream):
+        if dX is None:
+            dX = torch.empty((T, K), dtype=torch.bfloat16, device=dY.device)
+        if ws is None:
+            need = (qlora_int8_expert_bwd_workspace_size(T, E, N, K) if by_expert
+                    else qlora_int8_linear_bwd_workspace_size(T, N, K))
+            ws = _workspace(need, dY.device)
+    fn = "qlora_int8_expert_bwd" if by_expert else "qlora_int8_linear_bwd"
+    sizes = (_ptr(offsets), T, E, N, K) if by_expert else (T, N, K)
+    st = getattr(_get_lib(), fn)(_ptr(dY), *sizes, _ptr(w.codes), _ptr(w.scale), _ptr(dX), _ptr(ws), ws.numel(),
+                                 _stream(stream))
+    _check(fn, st)
+    return dX
+
+
+def qlora_int8_linear_fwd(X, w: Int8Rows, out_dtype=None, Y=None, ws=None, stream=None):
+    """Y = X W^T in 8-bit integers, scaled per token and output channel; bf16
+    by default.  X: M x K bf16, quantized by row on the way, or the Int8Rows
+    of tokens quantized before (for several linears on one input)."""
+    return _int8_fwd(X, w, None, out_dtype, Y, ws, stream)
+
+
+def qlora_int8_linear_bwd(dY, w: Int8Rows, dX=None, ws=None, stream=None):
+    """dX = dY W' (bf16) through the frozen weight W' = bf16(codes * scale)."""
+    return _int8_bwd(dY, w, None, dX, ws, stream)
+
+
+def qlora_int8_expert_fwd(X, w: Int8Rows, offsets, out_dtype=None, Y=None, ws=None, stream=None):
+    """qlora_int8_linear_fwd by expert: rows offsets[e] .. offsets[e + 1] - 1
+    of X use the weight w[e] (w: E x N x K; offsets: int32 [E + 1] on the
+    device).  Rows outside every range keep what Y held."""
+    if offsets is None:
+        raise ValueError("offsets must be an int32 tensor")
+    return _int8_fwd(X, w, offsets, out_dtype, Y, ws, stream)
+
+
+def qlora_int8_expert_bwd(dY, w: Int8Rows, offsets, dX=None, ws=None, stream=None):
+    """qlora_int8_linear_bwd by expert, with the rows of qlora_int8_expert_fwd."""
+    if offsets is None:
+        raise ValueError("offsets must be an int32 tensor")
+    return _int8_bwd(dY, w, offsets, dX, ws, stream)
 
 
 def qlora_debug_wait_timeout(limit_ns: int, stream=None) -> None:

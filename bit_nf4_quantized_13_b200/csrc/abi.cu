@@ -376,6 +376,126 @@ int qlora_int8_dequantize(const int8_t* codes, const float* c, int64_t numel, in
     return cuda_status(launch_int8_dequantize(codes, c, numel, block, out, as_stream(stream)));
 }
 
+}  // extern "C"
+
+// ---- the Int8 linear, dense (offsets == nullptr, E = 1) or by expert
+namespace {
+
+int check_int8(int64_t T, int E, int64_t N, int64_t K, bool by_expert, const int32_t* offsets) {
+    if (T < 0 || E < 1 || N < 1 || K < 1) return QLORA_ERR_INVALID_ARG;
+    if (by_expert && T > 0 && !ok_ptr(offsets)) return QLORA_ERR_INVALID_ARG;
+    if (K > QLORA_INT8_MAX_K || E > QLORA_MAX_EXPERTS || T >= (int64_t(1) << 30) || N >= (int64_t(1) << 30) ||
+        E * N >= (int64_t(1) << 31))
+        return QLORA_ERR_UNSUPPORTED;
+    return QLORA_OK;
+}
+
+// Workspace of the forward: the tokens' codes, then their scales.
+size_t int8_codes_bytes(int64_t T, int64_t K) { return align256(static_cast<size_t>(T) * int8_row_bytes(K)); }
+size_t int8_fwd_ws(int64_t T, int E, int64_t N, int64_t K) {
+    if (check_int8(T, E, N, K, false, nullptr) != QLORA_OK) return 0;
+    return int8_codes_bytes(T, K) + align256(static_cast<size_t>(T) * 4);
+}
+size_t int8_bwd_ws(int64_t T, int E, int64_t N, int64_t K) {
+    if (check_int8(T, E, N, K, false, nullptr) != QLORA_OK) return 0;
+    return 0;
+}
+
+// X != nullptr: bf16 tokens, quantized into the workspace first; else
+// x_codes and x_scale hold them.
+int int8_fwd(const uint16_t* X, const int8_t* x_codes, const float* x_scale, const int32_t* offsets, bool by_expert,
+             bool quantized, int64_t T, int E, int64_t N, int64_t K, const int8_t* w_codes, const float* w_scale,
+             void* Y, int out_dtype, void* ws, size_t ws_bytes, void* stream) {
+    const int st = check_int8(T, E, N, K, by_expert, offsets);
+    if (st != QLORA_OK) return st;
+    if (out_dtype != 0 && out_dtype != 1) return QLORA_ERR_INVALID_ARG;
+    if (!ok_ptr(w_codes) || !ok_ptr(w_scale)) return QLORA_ERR_INVALID_ARG;
+    if (T == 0) return QLORA_OK;
+    if (!ok_ptr(Y) || (quantized ? !ok_ptr(x_codes) || !ok_ptr(x_scale) : !ok_ptr(X))) return QLORA_ERR_INVALID_ARG;
+    if (!ws || !aligned16(ws) || ws_bytes < int8_fwd_ws(T, E, N, K)) return QLORA_ERR_WORKSPACE;
+    cudaStream_t cs = as_stream(stream);
+    cudaError_t e = cudaSuccess;
+    if (!quantized) {
+        int8_t* xc = static_cast<int8_t*>(ws);
+        float* xs = reinterpret_cast<float*>(xc + int8_codes_bytes(T, K));
+        e = launch_int8_rows(X, 1, T, K, xc, xs, nullptr, cs);
+        x_codes = xc;
+        x_scale = xs;
+    }
+    const Int8Weight w{w_codes, w_scale, E, N, K, int8_row_bytes(K)};
+    if (e == cudaSuccess) e = launch_int8_fwd(x_codes, x_scale, w, RowRanges{offsets, T}, Y, out_dtype, cs);
+    return cuda_status(e);
+}
+
+int int8_bwd(const uint16_t* dY, const int32_t* offsets, bool by_expert, int64_t T, int E, int64_t N, int64_t K,
+             const int8_t* w_codes, const float* w_scale, uint16_t* dX, void* ws, size_t ws_bytes, void* stream) {
+    const int st = check_int8(T, E, N, K, by_expert, offsets);
+    if (st != QLORA_OK) return st;
+    if (!ok_ptr(w_codes) || !ok_ptr(w_scale)) return QLORA_ERR_INVALID_ARG;
+    if (T == 0) return QLORA_OK;
+    if (!ok_ptr(dY) || !ok_ptr(dX)) return QLORA_ERR_INVALID_ARG;
+    if (!ws || !aligned16(ws) || ws_bytes < int8_bwd_ws(T, E, N, K)) return QLORA_ERR_WORKSPACE;
+    const Int8Weight w{w_codes, w_scale, E, N, K, int8_row_bytes(K)};
+    return cuda_status(launch_int8_dx(dY, w, RowRanges{offsets, T}, dX, as_stream(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int qlora_int8_quantize_rows(const void* x, int x_dtype, int64_t rows, int64_t K, int8_t* codes, float* scale,
+                             int32_t* status, void* stream) {
+    if (rows < 0 || K < 1 || (x_dtype != 0 && x_dtype != 1)) return QLORA_ERR_INVALID_ARG;
+    if (K > QLORA_INT8_MAX_K || rows >= (int64_t(1) << 31)) return QLORA_ERR_UNSUPPORTED;
+    if (status && (reinterpret_cast<uintptr_t>(status) & 3u)) return QLORA_ERR_INVALID_ARG;
+    if (rows == 0) return QLORA_OK;
+    if (!ok_ptr(x) || !ok_ptr(codes) || !ok_ptr(scale)) return QLORA_ERR_INVALID_ARG;
+    return cuda_status(launch_int8_rows(x, x_dtype, rows, K, codes, scale, status, as_stream(stream)));
+}
+
+size_t qlora_int8_linear_fwd_workspace_size(int64_t M, int64_t N, int64_t K) { return int8_fwd_ws(M, 1, N, K); }
+size_t qlora_int8_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K) { return int8_bwd_ws(M, 1, N, K); }
+size_t qlora_int8_expert_fwd_workspace_size(int64_t T, int E, int64_t N, int64_t K) { return int8_fwd_ws(T, E, N, K); }
+size_t qlora_int8_expert_bwd_workspace_size(int64_t T, int E, int64_t N, int64_t K) { return int8_bwd_ws(T, E, N, K); }
+
+int qlora_int8_linear_fwd(const uint16_t* X, int64_t M, int64_t N, int64_t K, const int8_t* w_codes,
+                          const float* w_scale, void* Y, int out_dtype, void* ws, size_t ws_bytes, void* stream) {
+    return int8_fwd(X, nullptr, nullptr, nullptr, false, false, M, 1, N, K, w_codes, w_scale, Y, out_dtype, ws,
+                    ws_bytes, stream);
+}
+
+int qlora_int8_matmul(const int8_t* x_codes, const float* x_scale, int64_t M, int64_t N, int64_t K,
+                      const int8_t* w_codes, const float* w_scale, void* Y, int out_dtype, void* ws,
+                      size_t ws_bytes, void* stream) {
+    return int8_fwd(nullptr, x_codes, x_scale, nullptr, false, true, M, 1, N, K, w_codes, w_scale, Y, out_dtype, ws,
+                    ws_bytes, stream);
+}
+
+int qlora_int8_linear_bwd(const uint16_t* dY, int64_t M, int64_t N, int64_t K, const int8_t* w_codes,
+                          const float* w_scale, uint16_t* dX, void* ws, size_t ws_bytes, void* stream) {
+    return int8_bwd(dY, nullptr, false, M, 1, N, K, w_codes, w_scale, dX, ws, ws_bytes, stream);
+}
+
+int qlora_int8_expert_fwd(const uint16_t* X, const int32_t* offsets, int64_t T, int E, int64_t N, int64_t K,
+                          const int8_t* w_codes, const float* w_scale, void* Y, int out_dtype, void* ws,
+                          size_t ws_bytes, void* stream) {
+    return int8_fwd(X, nullptr, nullptr, offsets, true, false, T, E, N, K, w_codes, w_scale, Y, out_dtype, ws,
+                    ws_bytes, stream);
+}
+
+int qlora_int8_expert_matmul(const int8_t* x_codes, const float* x_scale, const int32_t* offsets, int64_t T, int E,
+                             int64_t N, int64_t K, const int8_t* w_codes, const float* w_scale, void* Y,
+                             int out_dtype, void* ws, size_t ws_bytes, void* stream) {
+    return int8_fwd(nullptr, x_codes, x_scale, offsets, true, true, T, E, N, K, w_codes, w_scale, Y, out_dtype, ws,
+                    ws_bytes, stream);
+}
+
+int qlora_int8_expert_bwd(const uint16_t* dY, const int32_t* offsets, int64_t T, int E, int64_t N, int64_t K,
+                          const int8_t* w_codes, const float* w_scale, uint16_t* dX, void* ws, size_t ws_bytes,
+                          void* stream) {
+    return int8_bwd(dY, offsets, true, T, E, N, K, w_codes, w_scale, dX, ws, ws_bytes, stream);
+}
+
 int qlora_debug_wait_timeout(uint64_t limit_ns, void* stream) {
     if (limit_ns == 0 || limit_ns > kMaxSelftestWaitNs) return QLORA_ERR_INVALID_ARG;
     return cuda_status(launch_wait_selftest(limit_ns, as_stream(stream)));

@@ -35,6 +35,45 @@ cudaError_t launch_int8_quantize(const float* x, int64_t numel, int block, int8_
 cudaError_t launch_int8_dequantize(const int8_t* codes, const float* c, int64_t numel, int block, float* out,
                                    cudaStream_t stream);
 
+// int8_rows.cu -- Int8 absmax quantization of rows (eq. 1, one block per
+// row); x_dtype 0: fp32, 1: bf16.  Rows of codes are int8_row_bytes(K) apart.
+__host__ __device__ inline int64_t int8_row_bytes(int64_t K) { return (K + 15) / 16 * 16; }
+cudaError_t launch_int8_rows(const void* x, int x_dtype, int64_t rows, int64_t K, int8_t* codes, float* scale,
+                             int32_t* status, cudaStream_t stream);
+
+// The frozen Int8 weight of one linear (E = 1) or of E experts: E x N rows of
+// K codes, ld = int8_row_bytes(K) bytes apart, with one scale each.
+struct Int8Weight {
+    const int8_t* codes;
+    const float* scale;
+    int E;
+    int64_t N, K, ld;
+};
+
+// The rows of each expert among T token rows: expert e has rows
+// [offsets[e], offsets[e + 1]); offsets == nullptr: one weight, all rows.
+struct RowRanges {
+    const int32_t* offsets;
+    int64_t T;
+};
+
+// Expert e's rows.  Whatever the offsets hold, the range lies in [0, T].
+__device__ __forceinline__ void expert_rows(const RowRanges& rr, int e, int* lo, int* hi) {
+    const int T = static_cast<int>(rr.T);
+    *lo = 0;
+    *hi = T;
+    if (rr.offsets) {
+        *lo = min(max(rr.offsets[e], 0), T);
+        *hi = min(max(rr.offsets[e + 1], *lo), T);
+    }
+}
+
+// int8_gemm.cu -- the Int8 linear's products (out_dtype 0: fp32, 1: bf16)
+cudaError_t launch_int8_fwd(const int8_t* x_codes, const float* x_scale, const Int8Weight& w, const RowRanges& rr,
+                            void* out, int out_dtype, cudaStream_t stream);
+cudaError_t launch_int8_dx(const uint16_t* dY, const Int8Weight& w, const RowRanges& rr, uint16_t* dX,
+                           cudaStream_t stream);
+
 // The frozen NF4 weight W (N x K row-major) as the GEMM kernels see it.
 struct Nf4Weight {
     const uint8_t* codes;   // N*K/2 bytes

@@ -340,6 +340,92 @@ int qlora_int8_quantize(const float* x, int64_t numel, int block, int8_t* codes,
 int qlora_int8_dequantize(const int8_t* codes, const float* c, int64_t numel, int block, float* out,
                           void* stream);
 
+/* ------------------------------------------------------------------------
+ * The Int8 linear: a frozen weight and its tokens held as rows of Int8 codes
+ * with one fp32 scale each (eq. 1 with a block per row), multiplied in 8-bit
+ * integers; and the same product grouped by expert.
+ *
+ * Rows of codes are QLORA_INT8_ROW_BYTES(K) bytes apart: K codes, then zero
+ * codes up to a multiple of 16 bytes.  K <= QLORA_INT8_MAX_K keeps every
+ * 32-bit sum of products exact.
+ * --------------------------------------------------------------------- */
+#define QLORA_INT8_ROW_BYTES(K) (((K) + 15) / 16 * 16)
+#define QLORA_INT8_MAX_K 131072
+#define QLORA_MAX_EXPERTS 1024
+
+/*
+ * qlora_int8_quantize_rows -- for each of `rows` rows of K values (all steps
+ * IEEE fp32, round to nearest even, unfused):
+ *   a     = max |x| over the row
+ *   c     = RN32(127 / a)          (0 where a is 0 or c overflows: a < 3.8e-37)
+ *   code  = round_half_away_from_zero(RN32(c * x))      in [-127, 127]
+ *   scale = RN32(a / 127)          (0 where c is 0)
+ *   x       in : rows x K, fp32 (x_dtype 0) or bf16 bits (x_dtype 1)
+ *   codes  out: rows x QLORA_INT8_ROW_BYTES(K) int8;  scale out: rows fp32
+ *   status  out: nullable device int32, cleared to QLORA_OK then set to
+ *                QLORA_ERR_NONFINITE if x holds a NaN or Inf.
+ * A row holding a NaN or Inf gets codes 0 and scale NaN, so that it stays
+ * visible: every product with it is NaN, other rows are not touched.
+ * rows == 0 enqueues nothing.
+ */
+int qlora_int8_quantize_rows(const void* x, int x_dtype, int64_t rows, int64_t K, int8_t* codes, float* scale,
+                             int32_t* status, void* stream);
+
+/*
+ * qlora_int8_matmul -- the product of M tokens and N output channels, both
+ * as written by qlora_int8_quantize_rows:
+ *   Y[m][n] = out(RN32(RN32(RN32(sum_k x_codes[m][k] w_codes[n][k]) * x_scale[m]) * w_scale[n]))
+ * The sum is exact (32-bit integers); out is fp32 (out_dtype 0) or bf16 bits
+ * (out_dtype 1).  Y: M x N.  The workspace is that of qlora_int8_linear_fwd.
+ */
+int qlora_int8_matmul(const int8_t* x_codes, const float* x_scale, int64_t M, int64_t N, int64_t K,
+                      const int8_t* w_codes, const float* w_scale, void* Y, int out_dtype, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/*
+ * qlora_int8_linear_fwd -- the tokens X (M x K bf16) quantized by row, then
+ * qlora_int8_matmul.  1 <= N, 1 <= K <= QLORA_INT8_MAX_K, M >= 0; no
+ * alignment of N or K is asked for.
+ */
+size_t qlora_int8_linear_fwd_workspace_size(int64_t M, int64_t N, int64_t K);
+int qlora_int8_linear_fwd(const uint16_t* X, int64_t M, int64_t N, int64_t K, const int8_t* w_codes,
+                          const float* w_scale, void* Y, int out_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * qlora_int8_linear_bwd -- the input gradient through the frozen weight in
+ * the compute type (as the 4-bit linear's; there is no gradient for W, and
+ * the rounding of the tokens counts as the identity):
+ *   dX = bf16(dY W'),  W'[n][k] = bf16(RN32(w_codes[n][k] * w_scale[n]))
+ * fp32 accumulation.  dY: M x N bf16, dX: M x K bf16.
+ */
+size_t qlora_int8_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K);
+int qlora_int8_linear_bwd(const uint16_t* dY, int64_t M, int64_t N, int64_t K, const int8_t* w_codes,
+                          const float* w_scale, uint16_t* dX, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * qlora_int8_expert_fwd / _matmul / _bwd -- the three calls above grouped by
+ * expert: T token rows sorted by expert, E weights of N x K (w_codes: E x N
+ * rows of codes, w_scale: E x N).  offsets: E + 1 device int32, ascending;
+ * rows offsets[e] .. offsets[e + 1] - 1 use weight e (none where the two are
+ * equal).  Rows before offsets[0] and from offsets[E] on belong to no expert:
+ * their output rows are left as they were.  Nothing is read or written
+ * outside the T rows whatever the offsets hold (each is taken clamped to
+ * [0, T]; the outputs are unspecified where they are not ascending).
+ * 1 <= E <= QLORA_MAX_EXPERTS, else QLORA_ERR_UNSUPPORTED; T == 0 enqueues
+ * nothing.
+ */
+size_t qlora_int8_expert_fwd_workspace_size(int64_t T, int E, int64_t N, int64_t K);
+int qlora_int8_expert_fwd(const uint16_t* X, const int32_t* offsets, int64_t T, int E, int64_t N, int64_t K,
+                          const int8_t* w_codes, const float* w_scale, void* Y, int out_dtype, void* ws,
+                          size_t ws_bytes, void* stream);
+int qlora_int8_expert_matmul(const int8_t* x_codes, const float* x_scale, const int32_t* offsets, int64_t T, int E,
+                             int64_t N, int64_t K, const int8_t* w_codes, const float* w_scale, void* Y,
+                             int out_dtype, void* ws, size_t ws_bytes, void* stream);
+size_t qlora_int8_expert_bwd_workspace_size(int64_t T, int E, int64_t N, int64_t K);
+int qlora_int8_expert_bwd(const uint16_t* dY, const int32_t* offsets, int64_t T, int E, int64_t N, int64_t K,
+                          const int8_t* w_codes, const float* w_scale, uint16_t* dX, void* ws, size_t ws_bytes,
+                          void* stream);
+
 /*
  * qlora_debug_wait_timeout -- failure-detection self-test (no counterpart
  * in the paper).  Launches one single-thread kernel on `stream` whose

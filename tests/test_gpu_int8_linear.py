@@ -1,0 +1,374 @@
+"""GPU parity of the Int8 linear (rows of Int8 codes, a scale per token and
+output channel) and of its expert-grouped form against their definitions in
+64 bits: codes, scales and untouched rows bit for bit, products within the
+counted roundings.  Sizes from one row to several tiles, ragged row ranges,
+masked (empty) experts, non-finite rows, streams and captured graphs."""
+import pytest
+import torch
+
+import int8_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import bit_nf4_quantized_13_b200 as q  # noqa: E402
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def tokens(seed, M, K, spread=1.0):
+    x = torch.randn((M, K), generator=gen(seed), device="cuda") * spread
+    x[:, K // 2] *= 8  # an outlier feature
+    return x.to(torch.bfloat16)
+
+
+def weight(seed, *shape):
+    return q.qlora_int8_quantize_rows(torch.randn(shape, generator=gen(seed), device="cuda") * 0.02)
+
+
+def fwd_ref(X, w, e=None):
+    wc, ws = ref.weight_rows(w.codes, w.scale, w.shape)
+    if e is not None:
+        wc, ws = wc[e], ws[e]
+    xc, xs, _ = ref.quantize_rows(X)
+    return ref.forward(xc, xs, wc, ws)
+
+
+def compute_weight(w, e=None):
+    wc, ws = ref.weight_rows(w.codes, w.scale, w.shape)
+    return ref.compute_weight(wc, ws) if e is None else ref.compute_weight(wc[e], ws[e])
+
+
+# ----------------------------------------------------------------- quantizer
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,K", [(1, 1), (1, 5120), (3, 15), (5, 16), (2, 17), (9, 1024), (8, 1025), (7, 2048),
+                                    (1000, 333), (4, 2049), (3, 8192), (3, 8200), (2, 16385), (2, 40000),
+                                    (4096, 512)])
+def test_rows_match_the_definition(rows, K, dtype):
+    x = (torch.randn((rows, K), generator=gen(rows + K), device="cuda") * 3).to(dtype)
+    r = q.qlora_int8_quantize_rows(x)
+    c, s, _ = ref.quantize_rows(x)
+    assert torch.equal(r.codes[:, :K].double(), c)
+    assert torch.equal(r.scale.double(), s)
+    assert not r.codes[:, K:].any()  # the padding
+
+
+def test_rows_zero_tiny_huge_and_ties():
+    x = torch.zeros((9, 300), device="cuda")
+    x[1, 5] = 1e-38          # c overflows: a zero row
+    x[2, 7] = -4e-37         # just above: c = 127 / 4e-37 is finite
+    x[3] = 3.0e38
+    x[4] = -torch.finfo(torch.float32).max
+    x[5, :3] = torch.tensor([127.0, 0.5, -1.5], device="cuda")  # halves go away from zero
+    x[6] = 1e-45             # the smallest subnormal
+    x[7, 299] = 2.0
+    x[8] = -0.0
+    r = q.qlora_int8_quantize_rows(x)
+    c, s, _ = ref.quantize_rows(x)
+    assert torch.equal(r.codes[:, :300].double(), c) and torch.equal(r.scale.double(), s)
+    assert r.codes[5, :3].tolist() == [127, 1, -2]
+    assert r.scale[0].item() == 0 and r.scale[1].item() == 0 and r.scale[6].item() == 0
+
+
+@pytest.mark.parametrize("K", [40, 4096, 20001])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_nonfinite_are_marked_alone(K, dtype):
+    x = torch.randn((6, K), generator=gen(4), device="cuda").to(dtype)
+    st = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    q.qlora_int8_quantize_rows(x, status=st)
+    assert st.item() == 0
+    x[1, K - 1], x[3, 0], x[4, K // 2] = float("nan"), float("inf"), float("-inf")
+    r = q.qlora_int8_quantize_rows(x, status=st)
+    assert st.item() == 5
+    c, s, bad = ref.quantize_rows(x)
+    assert bad.tolist() == [False, True, False, True, True, False]
+    assert torch.equal(r.scale.isnan(), bad)
+    assert torch.equal(r.codes[:, :K].double(), c)  # codes 0 in the marked rows
+    assert torch.equal(r.scale[~bad].double(), s[~bad])
+
+
+# -------------------------------------------------------------- dense linear
+
+FWD_SIZES = [(1, 1, 1), (1, 64, 64), (1, 5120, 512), (2, 33, 100), (3, 16, 4096), (7, 257, 1111), (8, 1000, 64),
+             (9, 100, 5000), (15, 31, 48), (16, 512, 5120), (17, 130, 96), (31, 64, 1024), (33, 1003, 1111),
+             (64, 300, 640), (100, 128, 3), (128, 256, 128), (130, 4097, 192), (255, 257, 129), (257, 512, 2048),
+             (300, 1024, 8200), (512, 640, 384), (700, 333, 777), (1025, 1280, 4096), (2049, 2304, 1024)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", FWD_SIZES)
+def test_linear_fwd(M, N, K, dtype):
+    X, w = tokens(M + N, M, K), weight(K, N, K)
+    Y = q.qlora_int8_linear_fwd(X, w, out_dtype=dtype)
+    assert Y.dtype == dtype
+    R = fwd_ref(X, w)
+    ref.check_forward(Y, R, "Y")
+    # tokens quantized before give the same bytes
+    assert torch.equal(q.qlora_int8_linear_fwd(q.qlora_int8_quantize_rows(X), w, out_dtype=dtype), Y)
+    assert q.qlora_device_error() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 64, 64), (5, 100, 64), (16, 512, 1000), (33, 1003, 1111),
+                                   (64, 8, 640), (100, 3, 128), (130, 4097, 192), (255, 129, 257), (300, 1024, 520),
+                                   (512, 640, 384), (513, 72, 2049), (700, 333, 777), (1025, 1280, 2048),
+                                   (2049, 2304, 1024)])
+def test_linear_bwd(M, N, K):
+    dY, w = tokens(M * 3 + N, M, N, 0.01), weight(K + 1, N, K)
+    dX = q.qlora_int8_linear_bwd(dY, w)
+    ref.check_backward(dX, dY, compute_weight(w), "dX")
+    assert q.qlora_device_error() == 0
+
+
+def test_largest_codes_fill_the_integer_sum():
+    """K * 127^2 just below 2^31: the largest sums, positive and negative."""
+    K = 131072
+    w = q.qlora_int8_quantize_rows(torch.ones((70, K), device="cuda"))
+    for M in (1, 40, 300):
+        X = torch.ones((M, K), dtype=torch.bfloat16, device="cuda")
+        X[M // 2] = -1
+        Y = q.qlora_int8_linear_fwd(X, w, out_dtype=torch.float32)
+        ref.check_forward(Y, fwd_ref(X, w), f"M = {M}")
+
+
+@pytest.mark.parametrize("M", [4, 100, 600])
+def test_nonfinite_and_zero_rows_stay_alone(M):
+    N, K = 300, 640
+    X, w = tokens(M, M, K), weight(3, N, K)
+    clean = q.qlora_int8_linear_fwd(X, w)
+    bad = X.clone()
+    bad[1, 17], bad[M - 1, 0] = float("nan"), float("inf")
+    bad[2] = 0
+    Y = q.qlora_int8_linear_fwd(bad, w)
+    assert Y[1].isnan().all() and Y[M - 1].isnan().all()
+    assert not Y[2].any()
+    keep = [m for m in range(M) if m not in (1, 2, M - 1)]
+    assert torch.equal(Y[keep], clean[keep])
+    # a NaN output channel, and a NaN row of dY
+    w.scale[5] = float("nan")
+    Y = q.qlora_int8_linear_fwd(X, w)
+    assert Y[:, 5].isnan().all() and not Y[:, :5].isnan().any() and not Y[:, 6:].isnan().any()
+    w.scale[5] = 0.01
+    dY = tokens(7, M, N)
+    clean = q.qlora_int8_linear_bwd(dY, w)
+    dY[1, 3] = float("nan")
+    dX = q.qlora_int8_linear_bwd(dY, w)
+    assert dX[1].isnan().all()
+    keep = [m for m in range(M) if m != 1]
+    assert torch.equal(dX[keep], clean[keep])
+
+
+def test_small_and_large_scales_do_not_underflow_on_the_way():
+    X = tokens(1, 40, 256) * 1e-30
+    w = q.qlora_int8_quantize_rows(torch.randn((64, 256), generator=gen(2), device="cuda") * 1e25)
+    ref.check_forward(q.qlora_int8_linear_fwd(X, w), fwd_ref(X, w))
+    X = tokens(1, 40, 256) * 1e30
+    w = q.qlora_int8_quantize_rows(torch.randn((64, 256), generator=gen(2), device="cuda") * 1e-30)
+    ref.check_forward(q.qlora_int8_linear_fwd(X, w), fwd_ref(X, w))
+
+
+def test_gradient_of_the_dequantized_product_by_differences():
+    """The product with the dequantized weight is linear in X, so a difference
+    quotient along any direction is <dX, direction> up to roundings: dX is off
+    by at most 2^-8 relative per element plus the fp32 sum's error."""
+    M, N, K = 40, 264, 320
+    w, dY = weight(11, N, K), tokens(12, M, N, 0.1)
+    W = compute_weight(w)
+    dX = q.qlora_int8_linear_bwd(dY, w).double()
+    X = torch.randn((M, K), generator=gen(13), device="cuda", dtype=torch.float64)
+    for seed in range(4):
+        D = torch.randn((M, K), generator=gen(20 + seed), device="cuda", dtype=torch.float64)
+        loss = lambda t: (dY.double() * (t @ W.T)).sum()  # noqa: E731
+        diff = (loss(X + 0.5 * D) - loss(X - 0.5 * D)).item()
+        tol = (D.abs() * (dX.abs() * 1.01 * 2.0 ** -8 + 1.01 * N * 2.0 ** -23 * (dY.double().abs() @ W.abs()))).sum()
+        # the quotient itself: two float64 sums of M N terms
+        tol = tol.item() + 1e-9 * abs(loss(X).item()) + 1e-9
+        assert abs(diff - (dX * D).sum().item()) <= tol
+
+
+# --------------------------------------------------------------- by expert
+
+def offsets_of(counts, first=0):
+    off = [first]
+    for n in counts:
+        off.append(off[-1] + n)
+    return torch.tensor(off, dtype=torch.int32, device="cuda")
+
+
+EXPERT_CASES = [
+    # counts per expert, rows before, rows behind, N, K
+    ([1], 0, 0, 64, 64),
+    ([0], 0, 3, 100, 48),
+    ([3, 0, 5], 0, 0, 130, 257),
+    ([0, 0, 0, 2], 1, 2, 1003, 100),
+    ([1, 1, 1, 1, 1, 1, 1, 1], 0, 0, 256, 1024),
+    ([16, 17, 15, 1, 0, 33], 2, 9, 300, 333),
+    ([2, 3, 0, 40, 1], 0, 7, 512, 2048),
+    ([128, 64, 0, 1], 0, 0, 384, 128),
+    ([100, 300, 0, 257, 5], 3, 23, 1408, 512),
+    ([600, 0, 1, 511, 513], 0, 1, 520, 776),
+    ([0] * 60 + [700] + [0] * 3, 0, 0, 72, 640),
+    ([7] * 128, 0, 0, 96, 160),
+    ([0, 1] * 500, 5, 5, 17, 33),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("counts,before,behind,N,K", EXPERT_CASES)
+def test_expert_fwd(counts, before, behind, N, K, dtype):
+    E, T = len(counts), sum(counts) + before + behind
+    off = offsets_of(counts, before)
+    X, w = tokens(N + T, T, K), weight(K, E, N, K)
+    Y = torch.full((T, N), 7.0, dtype=dtype, device="cuda")
+    assert q.qlora_int8_expert_fwd(X, w, off, Y=Y) is Y
+    o = off.tolist()
+    for e in range(E):
+        if o[e + 1] > o[e]:
+            ref.check_forward(Y[o[e]:o[e + 1]], fwd_ref(X[o[e]:o[e + 1]], w, e), f"expert {e}")
+    assert (Y[:o[0]] == 7).all() and (Y[o[-1]:] == 7).all()
+    Y2 = torch.full((T, N), 7.0, dtype=dtype, device="cuda")
+    q.qlora_int8_expert_fwd(q.qlora_int8_quantize_rows(X), w, off, Y=Y2)
+    assert torch.equal(Y, Y2)
+    assert q.qlora_device_error() == 0
+
+
+@pytest.mark.parametrize("counts,before,behind,N,K", EXPERT_CASES)
+def test_expert_bwd(counts, before, behind, N, K):
+    E, T = len(counts), sum(counts) + before + behind
+    off = offsets_of(counts, before)
+    dY, w = tokens(N + T + 1, T, N, 0.01), weight(K + 2, E, N, K)
+    dX = torch.full((T, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert q.qlora_int8_expert_bwd(dY, w, off, dX=dX) is dX
+    o = off.tolist()
+    for e in range(E):
+        if o[e + 1] > o[e]:
+            ref.check_backward(dX[o[e]:o[e + 1]], dY[o[e]:o[e + 1]], compute_weight(w, e), f"expert {e}")
+    assert (dX[:o[0]] == 7).all() and (dX[o[-1]:] == 7).all()
+    assert q.qlora_device_error() == 0
+
+
+def test_experts_equal_the_dense_linear():
+    """Each expert's rows are exactly the dense call's on those rows: the
+    forward's sums are exact, so the bytes agree whatever kernel ran."""
+    counts, N, K = [40, 0, 3, 300], 640, 512
+    off = offsets_of(counts)
+    X, w = tokens(5, sum(counts), K), weight(6, len(counts), N, K)
+    Y = q.qlora_int8_expert_fwd(X, w, off)
+    o = off.tolist()
+    for e in range(len(counts)):
+        if counts[e]:
+            we = q.Int8Rows(w.codes[e].contiguous(), w.scale[e].contiguous(), (N, K))
+            assert torch.equal(Y[o[e]:o[e + 1]], q.qlora_int8_linear_fwd(X[o[e]:o[e + 1]].contiguous(), we))
+
+
+@pytest.mark.parametrize("off", [[0, 10 ** 6, 2 * 10 ** 6], [-5, 20, 10 ** 9], [30, 10, 50], [2 ** 31 - 1, -2 ** 31, 0]])
+def test_offsets_outside_the_rows_are_clamped(off):
+    """Offsets that no router writes stay inside the T rows: the guard rows on
+    both sides of the outputs keep their bytes."""
+    T, N, K = 50, 96, 64
+    w = weight(1, 2, N, K)
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+    for width, call in ((N, lambda t, o: q.qlora_int8_expert_fwd(t, w, offsets, Y=o)),
+                        (K, lambda t, o: q.qlora_int8_expert_bwd(t, w, offsets, dX=o))):
+        big = torch.full((3 * T, width), 7.0, dtype=torch.bfloat16, device="cuda")
+        call(tokens(2, T, K if width == N else N), big[T:2 * T])
+        torch.cuda.synchronize()
+        assert (big[:T] == 7).all() and (big[2 * T:] == 7).all()
+    assert q.qlora_device_error() == 0
+
+
+# ------------------------------------------------- streams, graphs, together
+
+def test_empty_batches():
+    w = weight(1, 64, 48)
+    X = torch.empty((0, 48), dtype=torch.bfloat16, device="cuda")
+    assert q.qlora_int8_linear_fwd(X, w).shape == (0, 64)
+    assert q.qlora_int8_linear_bwd(torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), w).shape == (0, 48)
+    r = q.qlora_int8_quantize_rows(X)
+    assert r.codes.shape == (0, 48) and r.scale.shape == (0,)
+    we = weight(1, 2, 64, 48)
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    assert q.qlora_int8_expert_fwd(X, we, off).shape == (0, 64)
+
+
+@pytest.mark.parametrize("M", [1, 16, 40, 500])
+def test_calls_on_another_stream(M):
+    N, K = 700, 1024
+    X, w, dY = tokens(M, M, K), weight(2, N, K), tokens(M + 1, M, N)
+    Y0, dX0 = q.qlora_int8_linear_fwd(X, w), q.qlora_int8_linear_bwd(dY, w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [(q.qlora_int8_linear_fwd(X, w, stream=side), q.qlora_int8_linear_bwd(dY, w, stream=side))
+            for _ in range(8)]
+    with torch.cuda.stream(side):
+        outs.append((q.qlora_int8_linear_fwd(X, w), q.qlora_int8_linear_bwd(dY, w)))
+    torch.cuda.current_stream().wait_stream(side)
+    for Y, dX in outs:
+        assert torch.equal(Y, Y0) and torch.equal(dX, dX0)
+
+
+@pytest.mark.parametrize("T", [12, 300, 1500])
+def test_graph_replays_follow_inputs_and_offsets(T):
+    E, N, K = 6, 520, 640
+    w = weight(3, E, N, K)
+    X, dY = tokens(1, T, K), tokens(2, T, N, 0.01)
+    off = offsets_of([T // 2, 0, T - T // 2, 0, 0, 0])
+    Y, dX = q.qlora_int8_expert_fwd(X, w, off), q.qlora_int8_expert_bwd(dY, w, off)  # first calls outside capture
+    Yd = q.qlora_int8_linear_fwd(X, q.Int8Rows(w.codes[0], w.scale[0], (N, K)))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q.qlora_int8_expert_fwd(X, w, off, Y=Y)
+        q.qlora_int8_expert_bwd(dY, w, off, dX=dX)
+        q.qlora_int8_linear_fwd(X, q.Int8Rows(w.codes[0], w.scale[0], (N, K)), Y=Yd)
+    for seed, counts in ((5, [0, T, 0, 0, 0, 0]), (6, [T // 6, T // 3, 0, 1, T - T // 6 - T // 3 - 1, 0])):
+        X.copy_(tokens(seed, T, K))
+        dY.copy_(tokens(seed + 10, T, N, 0.01))
+        off.copy_(offsets_of(counts))
+        for _ in range(2):
+            graph.replay()
+        o = off.tolist()
+        for e in range(E):
+            if counts[e]:
+                ref.check_forward(Y[o[e]:o[e + 1]], fwd_ref(X[o[e]:o[e + 1]], w, e), f"expert {e}")
+                ref.check_backward(dX[o[e]:o[e + 1]], dY[o[e]:o[e + 1]], compute_weight(w, e), f"expert {e}")
+        ref.check_forward(Yd, fwd_ref(X, w, 0), "dense")
+
+
+def test_an_expert_block_forward_and_back():
+    """Router order, gate and up on tokens quantized once, down, and the input
+    gradients of all three: each call against the definition on its own
+    inputs, rows of no expert untouched."""
+    T, E, H, F = 333, 5, 512, 776
+    g = gen(9)
+    choice = torch.randint(0, E + 1, (T,), generator=g, device="cuda")  # expert E: dropped tokens
+    order = torch.argsort(choice, stable=True)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[1:] = torch.bincount(choice, minlength=E + 1)[:E].cumsum(0).to(torch.int32)
+    o = off.tolist()
+    X = tokens(10, T, H)[order].contiguous()
+    gate, up, down = weight(1, E, F, H), weight(2, E, F, H), weight(3, E, H, F)
+    xq = q.qlora_int8_quantize_rows(X)
+    zeros = lambda n: torch.zeros((T, n), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    G, U = q.qlora_int8_expert_fwd(xq, gate, off, Y=zeros(F)), q.qlora_int8_expert_fwd(xq, up, off, Y=zeros(F))
+    A = (torch.nn.functional.silu(G.float()) * U.float()).to(torch.bfloat16)
+    Y = q.qlora_int8_expert_fwd(A, down, off, Y=zeros(H))
+    dY = tokens(12, T, H, 0.01)
+    dA = q.qlora_int8_expert_bwd(dY, down, off, dX=zeros(F))
+    sig = torch.sigmoid(G.float())
+    dU = (dA.float() * G.float() * sig).to(torch.bfloat16)
+    dG = (dA.float() * U.float() * sig * (1 + G.float() * (1 - sig))).to(torch.bfloat16)
+    dX = q.qlora_int8_expert_bwd(dG, gate, off, dX=zeros(H)), q.qlora_int8_expert_bwd(dU, up, off, dX=zeros(H))
+    for e in range(E):
+        s = slice(o[e], o[e + 1])
+        for got, x, w in ((G, X, gate), (U, X, up), (Y, A, down)):
+            ref.check_forward(got[s], fwd_ref(x[s], w, e), f"expert {e}")
+        for got, d, w in ((dA, dY, down), (dX[0], dG, gate), (dX[1], dU, up)):
+            ref.check_backward(got[s], d[s], compute_weight(w, e), f"expert {e}")
+    for t in (G, U, Y, dA, *dX):
+        assert not t[o[-1]:].any()

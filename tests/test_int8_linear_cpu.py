@@ -1,0 +1,165 @@
+"""The Int8 linear's refusals and marshalling on the CPU: argument errors of
+the C entry points (nothing is launched on these paths), and the Python
+binding's checks with a recorder in the library's place."""
+import pytest
+import torch
+
+import bit_nf4_quantized_13_b200 as q
+from test_binding_cpu import fake  # noqa: F401  (the recorder fixture)
+
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from bit_nf4_quantized_13_b200 import build
+    build.build()
+    return q.lib
+
+
+P = 1 << 20  # a 16-byte-aligned stand-in address; never dereferenced on these paths
+BIG = 1 << 40
+
+
+def test_quantize_rows_refusals(lib):
+    f = lib.qlora_int8_quantize_rows
+    assert f(P, 0, -1, 8, P, P, None, None) == INVALID
+    assert f(P, 0, 4, 0, P, P, None, None) == INVALID
+    assert f(P, 2, 4, 8, P, P, None, None) == INVALID            # unknown dtype
+    assert f(P, 0, 4, 131073, P, P, None, None) == UNSUPPORTED
+    assert f(P, 0, 1 << 31, 8, P, P, None, None) == UNSUPPORTED
+    assert f(None, 1, 4, 8, P, P, None, None) == INVALID
+    assert f(P + 2, 1, 4, 8, P, P, None, None) == INVALID
+    assert f(P, 1, 4, 8, P + 8, P, None, None) == INVALID
+    assert f(P, 1, 4, 8, P, None, None, None) == INVALID
+    assert f(P, 1, 4, 8, P, P, P + 2, None) == INVALID           # misaligned status
+    assert f(None, 1, 0, 8, None, None, None, None) == OK        # no rows: nothing enqueued
+
+
+def test_linear_refusals(lib):
+    for f, x in ((lib.qlora_int8_linear_fwd, (P,)), (lib.qlora_int8_matmul, (P, P))):
+        assert f(*x, -1, 8, 8, P, P, P, 1, P, BIG, None) == INVALID
+        assert f(*x, 4, 0, 8, P, P, P, 1, P, BIG, None) == INVALID
+        assert f(*x, 4, 8, 0, P, P, P, 1, P, BIG, None) == INVALID
+        assert f(*x, 4, 8, 131073, P, P, P, 1, P, BIG, None) == UNSUPPORTED
+        assert f(*x, 1 << 30, 8, 8, P, P, P, 1, P, BIG, None) == UNSUPPORTED
+        assert f(*x, 4, 1 << 30, 8, P, P, P, 1, P, BIG, None) == UNSUPPORTED
+        assert f(*x, 4, 8, 8, P, P, P, 2, P, BIG, None) == INVALID   # unknown output type
+        assert f(*x, 4, 8, 8, P, P, P, -1, P, BIG, None) == INVALID
+        assert f(*x, 4, 8, 8, None, P, P, 1, P, BIG, None) == INVALID
+        assert f(*x, 4, 8, 8, P, P + 4, P, 1, P, BIG, None) == INVALID
+        assert f(*x, 4, 8, 8, P, P, None, 1, P, BIG, None) == INVALID
+        assert f(*(None,) * len(x), 4, 8, 8, P, P, P, 1, P, BIG, None) == INVALID
+        assert f(*x, 4, 8, 8, P, P, P, 1, None, BIG, None) == WORKSPACE
+        assert f(*x, 4, 8, 8, P, P, P, 1, P, 100, None) == WORKSPACE
+        assert f(*(None,) * len(x), 0, 8, 8, P, P, None, 1, None, 0, None) == OK  # no tokens
+    f = lib.qlora_int8_linear_bwd
+    assert f(P, -1, 8, 8, P, P, P, P, BIG, None) == INVALID
+    assert f(P, 4, 8, 131073, P, P, P, P, BIG, None) == UNSUPPORTED
+    assert f(None, 4, 8, 8, P, P, P, P, BIG, None) == INVALID
+    assert f(P, 4, 8, 8, P, P, P + 2, P, BIG, None) == INVALID
+    assert f(P, 4, 8, 8, None, P, P, P, BIG, None) == INVALID
+    assert f(P, 4, 8, 8, P, P, P, None, 0, None) == WORKSPACE
+    assert f(None, 0, 8, 8, P, P, None, None, 0, None) == OK
+
+
+def test_expert_refusals(lib):
+    for f, x in ((lib.qlora_int8_expert_fwd, (P,)), (lib.qlora_int8_expert_matmul, (P, P))):
+        assert f(*x, P, 4, 0, 8, 8, P, P, P, 1, P, BIG, None) == INVALID
+        assert f(*x, P, 4, 1025, 8, 8, P, P, P, 1, P, BIG, None) == UNSUPPORTED
+        assert f(*x, P, 4, 1024, 1 << 22, 8, P, P, P, 1, P, BIG, None) == UNSUPPORTED  # E N >= 2^31
+        assert f(*x, None, 4, 2, 8, 8, P, P, P, 1, P, BIG, None) == INVALID            # no offsets
+        assert f(*x, P + 4, 4, 2, 8, 8, P, P, P, 1, P, BIG, None) == INVALID
+        assert f(*x, P, 4, 2, 8, 8, P, P, P, 1, P, 0, None) == WORKSPACE
+        assert f(*x, None, 0, 2, 8, 8, P, P, None, 1, None, 0, None) == OK
+    f = lib.qlora_int8_expert_bwd
+    assert f(P, None, 4, 2, 8, 8, P, P, P, P, BIG, None) == INVALID
+    assert f(P, P, 4, 1025, 8, 8, P, P, P, P, BIG, None) == UNSUPPORTED
+    assert f(P, P, 4, 2, 8, 8, P, P, None, P, BIG, None) == INVALID
+    assert f(P, P, 0, 2, 8, 8, P, P, None, None, 0, None) == OK
+
+
+def test_workspace_sizes(lib):
+    # the tokens' codes (rows of 16-byte multiples) and scales at least
+    assert q.qlora_int8_linear_fwd_workspace_size(100, 8, 33) >= 100 * 48 + 400
+    assert q.qlora_int8_expert_fwd_workspace_size(100, 4, 8, 33) >= 100 * 48 + 400
+    assert q.qlora_int8_linear_fwd_workspace_size(4, 8, 131073) == 0
+    assert q.qlora_int8_expert_bwd_workspace_size(4, 1025, 8, 8) == 0
+
+
+def bf16(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def test_operands_reach_the_library(fake):  # noqa: F811
+    w, we = q.alloc_int8_rows((24, 33), "cpu"), q.alloc_int8_rows((3, 24, 33), "cpu")
+    assert w.codes.shape == (24, 48) and we.codes.shape == (3, 24, 48) and we.scale.shape == (3, 24)
+    assert w.nbytes() == 24 * 48 + 24 * 4
+    off = torch.zeros(4, dtype=torch.int32)
+    Y = q.qlora_int8_linear_fwd(bf16(5, 33), w)
+    name, args = fake.calls[-1]
+    assert name == "qlora_int8_linear_fwd" and args[1:4] == (5, 24, 33) and args[7] == 1
+    assert Y.shape == (5, 24) and Y.dtype == torch.bfloat16
+    Y = q.qlora_int8_linear_fwd(q.alloc_int8_rows((5, 33), "cpu"), w, out_dtype=torch.float32)
+    name, args = fake.calls[-1]
+    assert name == "qlora_int8_matmul" and args[2:5] == (5, 24, 33) and args[8] == 0 and Y.dtype == torch.float32
+    q.qlora_int8_linear_fwd(bf16(5, 33), w, Y=torch.zeros(5, 24))  # the output's own type is taken
+    assert fake.calls[-1][1][7] == 0
+    assert q.qlora_int8_linear_bwd(bf16(5, 24), w).shape == (5, 33)
+    assert fake.calls[-1][0] == "qlora_int8_linear_bwd" and fake.calls[-1][1][1:4] == (5, 24, 33)
+    assert q.qlora_int8_expert_fwd(bf16(5, 33), we, off).shape == (5, 24)
+    assert fake.calls[-1][0] == "qlora_int8_expert_fwd" and fake.calls[-1][1][2:6] == (5, 3, 24, 33)
+    q.qlora_int8_expert_fwd(q.alloc_int8_rows((5, 33), "cpu"), we, off)
+    assert fake.calls[-1][0] == "qlora_int8_expert_matmul" and fake.calls[-1][1][3:7] == (5, 3, 24, 33)
+    assert q.qlora_int8_expert_bwd(bf16(5, 24), we, off).shape == (5, 33)
+    assert fake.calls[-1][0] == "qlora_int8_expert_bwd" and fake.calls[-1][1][2:6] == (5, 3, 24, 33)
+    r = q.qlora_int8_quantize_rows(torch.zeros(2, 3, 33))
+    assert r.shape == (2, 3, 33) and r.codes.shape == (2, 3, 48)
+    assert fake.calls[-1][0] == "qlora_int8_quantize_rows" and fake.calls[-1][1][1:4] == (0, 6, 33)
+
+
+def test_disagreeing_operands_are_refused(fake):  # noqa: F811
+    w, we = q.alloc_int8_rows((24, 33), "cpu"), q.alloc_int8_rows((3, 24, 33), "cpu")
+    off = torch.zeros(4, dtype=torch.int32)
+    X, dY = bf16(5, 33), bf16(5, 24)
+    bad = [
+        lambda: q.qlora_int8_linear_fwd(bf16(5, 48), w),                            # K
+        lambda: q.qlora_int8_linear_fwd(X.float(), w),                              # dtype
+        lambda: q.qlora_int8_linear_fwd(X, we),                                     # a weight of experts
+        lambda: q.qlora_int8_linear_fwd(X[0], w),                                   # not 2-D
+        lambda: q.qlora_int8_linear_fwd(X, w, out_dtype=torch.float16),
+        lambda: q.qlora_int8_linear_fwd(X, w, Y=bf16(5, 25)),
+        lambda: q.qlora_int8_linear_fwd(X, w, out_dtype=torch.float32, Y=bf16(5, 24)),
+        lambda: q.qlora_int8_linear_fwd(X, q.Int8Rows(w.codes[:, :33], w.scale, (24, 33))),   # rows not padded
+        lambda: q.qlora_int8_linear_fwd(X, q.Int8Rows(w.codes, w.scale[:5], (24, 33))),
+        lambda: q.qlora_int8_linear_fwd(X, q.Int8Rows(w.codes.to(torch.uint8), w.scale, (24, 33))),
+        lambda: q.qlora_int8_linear_fwd(X, q.Int8Rows(w.codes, w.scale.double(), (24, 33))),
+        lambda: q.qlora_int8_linear_fwd(q.alloc_int8_rows((5, 34), "cpu"), w),
+        lambda: q.qlora_int8_linear_bwd(X, w),                                      # N
+        lambda: q.qlora_int8_linear_bwd(q.alloc_int8_rows((5, 24), "cpu"), w),      # quantized gradients
+        lambda: q.qlora_int8_linear_bwd(dY, w, dX=bf16(5, 48)),
+        lambda: q.qlora_int8_linear_bwd(dY, w, dX=torch.zeros(5, 33)),
+        lambda: q.qlora_int8_expert_fwd(X, w, off),                                 # a dense weight
+        lambda: q.qlora_int8_expert_fwd(X, we, off[:3]),
+        lambda: q.qlora_int8_expert_fwd(X, we, off.long()),
+        lambda: q.qlora_int8_expert_fwd(X, we, None),
+        lambda: q.qlora_int8_expert_bwd(dY, we, None),
+        lambda: q.qlora_int8_expert_bwd(dY, we, off.float()),
+        lambda: q.qlora_int8_quantize_rows(X.half()),
+        lambda: q.qlora_int8_quantize_rows(X[0]),
+        lambda: q.qlora_int8_quantize_rows(bf16(5, 0)),
+        lambda: q.qlora_int8_quantize_rows(X, out=q.alloc_int8_rows((5, 34), "cpu")),
+        lambda: q.qlora_int8_quantize_rows(X, status=torch.zeros(1, dtype=torch.int64)),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    assert fake.calls == [], "nothing may reach the library"
+
+
+def test_library_status_becomes_an_exception(fake):  # noqa: F811
+    fake.status = 2
+    with pytest.raises(q.QloraError) as e:
+        q.qlora_int8_linear_fwd(bf16(5, 33), q.alloc_int8_rows((24, 33), "cpu"))
+    assert e.value.status == 2
