@@ -353,7 +353,8 @@ int qlora_device_error(int reset) {
     const int a = pair_device_error(reset);
     const int b = lora_device_error(reset);
     const int c = gemv_device_error(reset);
-    return a != QLORA_OK ? a : b != QLORA_OK ? b : c;
+    const int d = int8_device_error(reset);
+    return a != QLORA_OK ? a : b != QLORA_OK ? b : c != QLORA_OK ? c : d;
 }
 
 int qlora_int8_quantize(const float* x, int64_t numel, int block, int8_t* codes, float* c, int32_t* status,
@@ -390,11 +391,11 @@ int check_int8(int64_t T, int E, int64_t N, int64_t K, bool by_expert, const int
     return QLORA_OK;
 }
 
-// Workspace of the forward: the tokens' codes, then their scales.
+// Workspace of the forward: the tokens' codes, their scales, the product's.
 size_t int8_codes_bytes(int64_t T, int64_t K) { return align256(static_cast<size_t>(T) * int8_row_bytes(K)); }
 size_t int8_fwd_ws(int64_t T, int E, int64_t N, int64_t K) {
     if (check_int8(T, E, N, K, false, nullptr) != QLORA_OK) return 0;
-    return int8_codes_bytes(T, K) + align256(static_cast<size_t>(T) * 4);
+    return int8_codes_bytes(T, K) + align256(static_cast<size_t>(T) * 4) + int8_pair_workspace(T);
 }
 size_t int8_bwd_ws(int64_t T, int E, int64_t N, int64_t K) {
     if (check_int8(T, E, N, K, false, nullptr) != QLORA_OK) return 0;
@@ -413,18 +414,23 @@ int int8_fwd(const uint16_t* X, const int8_t* x_codes, const float* x_scale, con
     if (T == 0) return QLORA_OK;
     if (!ok_ptr(Y) || (quantized ? !ok_ptr(x_codes) || !ok_ptr(x_scale) : !ok_ptr(X))) return QLORA_ERR_INVALID_ARG;
     if (!ws || !aligned16(ws) || ws_bytes < int8_fwd_ws(T, E, N, K)) return QLORA_ERR_WORKSPACE;
+    const Int8Weight w{w_codes, w_scale, E, N, K, int8_row_bytes(K)};
+    if (!int8_pair_supported(T, w)) return QLORA_ERR_UNSUPPORTED;
     cudaStream_t cs = as_stream(stream);
-    cudaError_t e = cudaSuccess;
-    if (!quantized) {
-        int8_t* xc = static_cast<int8_t*>(ws);
-        float* xs = reinterpret_cast<float*>(xc + int8_codes_bytes(T, K));
-        e = launch_int8_rows(X, 1, T, K, xc, xs, nullptr, cs);
+    int8_t* xc = static_cast<int8_t*>(ws);
+    float* xs = reinterpret_cast<float*>(xc + int8_codes_bytes(T, K));
+    int* gws = reinterpret_cast<int*>(reinterpret_cast<char*>(xs) + align256(static_cast<size_t>(T) * 4));
+    cudaError_t e;
+    if (quantized) {
+        e = cudaMemsetAsync(gws, 0, int8_pair_counter_bytes(), cs);
+    } else {
+        e = launch_int8_rows(X, 1, T, K, xc, xs, nullptr, cs, gws, static_cast<int>(int8_pair_counter_bytes() / 4));
         x_codes = xc;
         x_scale = xs;
     }
-    const Int8Weight w{w_codes, w_scale, E, N, K, int8_row_bytes(K)};
-    if (e == cudaSuccess) e = launch_int8_fwd(x_codes, x_scale, w, RowRanges{offsets, T}, Y, out_dtype, cs);
-    return cuda_status(e);
+    if (e == cudaSuccess)
+        e = launch_int8_fwd_pair(x_codes, x_scale, w, RowRanges{offsets, T}, Y, out_dtype, gws, cs, !quantized);
+    return pair_status(e);
 }
 
 int int8_bwd(const uint16_t* dY, const int32_t* offsets, bool by_expert, int64_t T, int E, int64_t N, int64_t K,

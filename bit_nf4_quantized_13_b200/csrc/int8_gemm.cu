@@ -1,8 +1,6 @@
-// int8_gemm.cu -- the Int8 linear's two products on the CUDA cores, dense or
-// grouped by expert (rows [offsets[e], offsets[e + 1]) of the tokens use
-// weight e):
+// int8_gemm.cu -- the Int8 linear's input gradient on the CUDA cores, dense
+// or grouped by expert (rows [offsets[e], offsets[e + 1]) of dY use weight e):
 //
-//   Y[m][n]  = (sum_k xq[m][k] wq[n][k]) * sx[m] * sw[n]      integer sums
 //   dX[m][k] = sum_n dY[m][n] * bf16(RN32(wq[n][k] * sw[n]))  fp32 sums
 #include "common.cuh"
 #include "kernels.h"
@@ -12,52 +10,6 @@ namespace {
 
 constexpr int kTile = 64;   // outputs of a block: 64 x 64, 4 x 4 a thread
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ void store_out(void* out, int64_t i, float v, int out_dtype) {
-    if (out_dtype == 0)
-        static_cast<float*>(out)[i] = v;
-    else
-        static_cast<uint16_t*>(out)[i] = f32_to_bf16_bits(v);
-}
-
-__global__ void __launch_bounds__(kThreads)
-k_int8_fwd(const int8_t* __restrict__ xc, const float* __restrict__ xs, const Int8Weight w, const RowRanges rr,
-           void* out, int out_dtype) {
-    __shared__ int sx[kTile][17], sw[kTile][17];  // 64 bytes of contraction as 16 words, one word of padding
-    int lo, hi;
-    expert_rows(rr, blockIdx.z, &lo, &hi);
-    const int64_t m0 = lo + static_cast<int64_t>(blockIdx.y) * kTile;
-    if (m0 >= hi) return;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    const int8_t* wc = w.codes + static_cast<int64_t>(blockIdx.z) * w.N * w.ld;
-    const float* ws = w.scale + static_cast<int64_t>(blockIdx.z) * w.N;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    int acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < w.ld; k0 += 64) {
-        for (int i = threadIdx.x; i < kTile * 16; i += kThreads) {
-            const int r = i / 16;
-            const int64_t k = k0 + (i % 16) * 4;
-            sx[r][i % 16] = (m0 + r < hi && k < w.ld) ? *reinterpret_cast<const int*>(xc + (m0 + r) * w.ld + k) : 0;
-            sw[r][i % 16] = (n0 + r < w.N && k < w.ld) ? *reinterpret_cast<const int*>(wc + (n0 + r) * w.ld + k) : 0;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(sx[ty + 16 * i][kk], sw[tx + 16 * j][kk], acc[i][j]);
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m < hi && n < w.N)
-                store_out(out, m * w.N + n, __fmul_rn(__fmul_rn(__int2float_rn(acc[i][j]), xs[m]), ws[n]), out_dtype);
-        }
-}
 
 __global__ void __launch_bounds__(kThreads)
 k_int8_dx(const uint16_t* __restrict__ dY, const Int8Weight w, const RowRanges rr, uint16_t* __restrict__ dX) {
@@ -105,13 +57,6 @@ dim3 grid_for(int64_t cols, const RowRanges& rr, int E) {
 }
 
 }  // namespace
-
-cudaError_t launch_int8_fwd(const int8_t* x_codes, const float* x_scale, const Int8Weight& w, const RowRanges& rr,
-                            void* out, int out_dtype, cudaStream_t st) {
-    k_int8_fwd<<<grid_for(w.N, rr, w.E), kThreads, 0, st>>>(x_codes, x_scale, w, rr, out, out_dtype);
-    note_launches(1);
-    return cudaGetLastError();
-}
 
 cudaError_t launch_int8_dx(const uint16_t* dY, const Int8Weight& w, const RowRanges& rr, uint16_t* dX,
                            cudaStream_t st) {

@@ -103,7 +103,10 @@ __device__ __forceinline__ void encode(const V& v, float c, int8_t* out) {
 template <typename T, bool kAligned, int kGroup>
 __global__ void __launch_bounds__(kThreads)
 k_int8_rows(const T* __restrict__ x, int64_t rows, int64_t K, int64_t ld, int8_t* __restrict__ codes,
-            float* __restrict__ scale, int* __restrict__ status) {
+            float* __restrict__ scale, int* __restrict__ status, int* __restrict__ zero, int n_zero) {
+    sm100::grid_launch_dependents();
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < n_zero; i += kThreads) zero[i] = 0;
     using V = RowVec<T, kAligned>;
     constexpr int kRows = kThreads / kGroup;
     const int tid = threadIdx.x % kGroup, lane = threadIdx.x & 31;
@@ -157,14 +160,15 @@ k_int8_rows(const T* __restrict__ x, int64_t rows, int64_t K, int64_t ld, int8_t
 
 template <typename T, bool kAligned>
 cudaError_t rows_launch(const T* x, int64_t rows, int64_t K, int64_t ld, int8_t* codes, float* scale, int* status,
-                        cudaStream_t st) {
+                        int* zero, int n_zero, cudaStream_t st) {
     constexpr int kPer = RowVec<T, kAligned>::kPer;
     if (ld <= 32 * kVecs * kPer) {
         const int64_t grid = ceil_div(rows, kThreads / 32);
-        k_int8_rows<T, kAligned, 32><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(x, rows, K, ld, codes, scale, status);
+        k_int8_rows<T, kAligned, 32><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(x, rows, K, ld, codes, scale, status,
+                                                                                      zero, n_zero);
     } else {
         k_int8_rows<T, kAligned, kThreads><<<static_cast<unsigned>(rows), kThreads, 0, st>>>(x, rows, K, ld, codes, scale,
-                                                                                          status);
+                                                                                          status, zero, n_zero);
     }
     note_launches(1);
     return cudaGetLastError();
@@ -173,7 +177,7 @@ cudaError_t rows_launch(const T* x, int64_t rows, int64_t K, int64_t ld, int8_t*
 }  // namespace
 
 cudaError_t launch_int8_rows(const void* x, int x_dtype, int64_t rows, int64_t K, int8_t* codes, float* scale,
-                             int32_t* status, cudaStream_t st) {
+                             int32_t* status, cudaStream_t st, int* zero, int n_zero) {
     int* flag = reinterpret_cast<int*>(status);
     if (flag) {
         const cudaError_t e = cudaMemsetAsync(flag, 0, sizeof(int), st);
@@ -182,12 +186,12 @@ cudaError_t launch_int8_rows(const void* x, int x_dtype, int64_t rows, int64_t K
     const int64_t ld = int8_row_bytes(K);
     if (x_dtype == 0) {
         const float* p = static_cast<const float*>(x);
-        return K % 4 == 0 ? rows_launch<float, true>(p, rows, K, ld, codes, scale, flag, st)
-                          : rows_launch<float, false>(p, rows, K, ld, codes, scale, flag, st);
+        return K % 4 == 0 ? rows_launch<float, true>(p, rows, K, ld, codes, scale, flag, zero, n_zero, st)
+                          : rows_launch<float, false>(p, rows, K, ld, codes, scale, flag, zero, n_zero, st);
     }
     const uint16_t* p = static_cast<const uint16_t*>(x);
-    return K % 8 == 0 ? rows_launch<uint16_t, true>(p, rows, K, ld, codes, scale, flag, st)
-                      : rows_launch<uint16_t, false>(p, rows, K, ld, codes, scale, flag, st);
+    return K % 8 == 0 ? rows_launch<uint16_t, true>(p, rows, K, ld, codes, scale, flag, zero, n_zero, st)
+                      : rows_launch<uint16_t, false>(p, rows, K, ld, codes, scale, flag, zero, n_zero, st);
 }
 
 }  // namespace qlora

@@ -37,9 +37,11 @@ cudaError_t launch_int8_dequantize(const int8_t* codes, const float* c, int64_t 
 
 // int8_rows.cu -- Int8 absmax quantization of rows (eq. 1, one block per
 // row); x_dtype 0: fp32, 1: bf16.  Rows of codes are int8_row_bytes(K) apart.
+// Also zeroes n_zero ints at `zero` (the product's counters), and lets a
+// dependent launch start early.
 __host__ __device__ inline int64_t int8_row_bytes(int64_t K) { return (K + 15) / 16 * 16; }
 cudaError_t launch_int8_rows(const void* x, int x_dtype, int64_t rows, int64_t K, int8_t* codes, float* scale,
-                             int32_t* status, cudaStream_t stream);
+                             int32_t* status, cudaStream_t stream, int* zero = nullptr, int n_zero = 0);
 
 // The frozen Int8 weight of one linear (E = 1) or of E experts: E x N rows of
 // K codes, ld = int8_row_bytes(K) bytes apart, with one scale each.
@@ -68,9 +70,19 @@ __device__ __forceinline__ void expert_rows(const RowRanges& rr, int e, int* lo,
     }
 }
 
-// int8_gemm.cu -- the Int8 linear's products (out_dtype 0: fp32, 1: bf16)
-cudaError_t launch_int8_fwd(const int8_t* x_codes, const float* x_scale, const Int8Weight& w, const RowRanges& rr,
-                            void* out, int out_dtype, cudaStream_t stream);
+// int8_pair_sm100.cu -- the forward on the tensor cores, on pairs of SMs
+// (out_dtype 0: fp32, 1: bf16).  The workspace's first
+// int8_pair_counter_bytes() must be zero when it starts; `dependent`: the
+// launch before it on the stream is the row quantizer, which it may overlap.
+bool int8_pair_supported(int64_t T, const Int8Weight& w);
+size_t int8_pair_counter_bytes();
+size_t int8_pair_workspace(int64_t T);
+cudaError_t launch_int8_fwd_pair(const int8_t* x_codes, const float* x_scale, const Int8Weight& w,
+                                 const RowRanges& rr, void* out, int out_dtype, void* ws, cudaStream_t stream,
+                                 bool dependent);
+int int8_device_error(int reset);
+
+// int8_gemm.cu -- the input gradient
 cudaError_t launch_int8_dx(const uint16_t* dY, const Int8Weight& w, const RowRanges& rr, uint16_t* dX,
                            cudaStream_t stream);
 

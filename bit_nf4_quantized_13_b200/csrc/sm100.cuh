@@ -174,6 +174,16 @@ __device__ __forceinline__ void mma_bf16_ss_pair(uint32_t d_tmem, uint64_t a_des
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// D (tmem, int32, both CTAs) (+)= A (smem, 256 x 32 bytes over the pair) * B (smem, N x 32 bytes over the pair)^T
+__device__ __forceinline__ void mma_i8_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 // Arrives once on the mbarrier at the same shared-memory offset `bar` in
 // every CTA of `cta_mask` when all pair MMAs issued so far by this thread
 // have completed.
@@ -214,6 +224,16 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn_major =
            | (1u << 10)                               // B format: bf16
            | (static_cast<uint32_t>(a_mn_major) << 15)  // A major
            | (static_cast<uint32_t>(b_mn_major) << 16)  // B major
+           | (static_cast<uint32_t>(N >> 3) << 17)    // N / 8
+           | (static_cast<uint32_t>(M >> 4) << 24);   // M / 16
+}
+
+// Instruction descriptor, kind::i8: int32 accumulator (no saturation),
+// signed 8-bit A and B, both K-major, shape M x N.
+__host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
+    return (2u << 4)                                  // D format: s32
+           | (1u << 7)                                // A format: s8
+           | (1u << 10)                               // B format: s8
            | (static_cast<uint32_t>(N >> 3) << 17)    // N / 8
            | (static_cast<uint32_t>(M >> 4) << 24);   // M / 16
 }
