@@ -85,12 +85,12 @@ def _load() -> ctypes.CDLL:
         "qlora_int8_linear_fwd_workspace_size": (sz, [i64, i64, i64]),
         "qlora_int8_linear_bwd_workspace_size": (sz, [i64, i64, i64]),
         "qlora_int8_linear_fwd": (i32, [vp, i64, i64, i64, vp, vp, vp, i32, vp, sz, vp]),
-        "qlora_int8_matmul": (i32, [vp, vp, i64, i64, i64, vp, vp, vp, i32, vp, sz, vp]),
+        "qlora_int8_matmul": (i32, [vp, vp, i64, i64, i64, vp, vp, vp, i32, vp]),
         "qlora_int8_linear_bwd": (i32, [vp, i64, i64, i64, vp, vp, vp, vp, sz, vp]),
         "qlora_int8_expert_fwd_workspace_size": (sz, [i64, i32, i64, i64]),
         "qlora_int8_expert_bwd_workspace_size": (sz, [i64, i32, i64, i64]),
         "qlora_int8_expert_fwd": (i32, [vp, vp, i64, i32, i64, i64, vp, vp, vp, i32, vp, sz, vp]),
-        "qlora_int8_expert_matmul": (i32, [vp, vp, vp, i64, i32, i64, i64, vp, vp, vp, i32, vp, sz, vp]),
+        "qlora_int8_expert_matmul": (i32, [vp, vp, vp, i64, i32, i64, i64, vp, vp, vp, i32, vp]),
         "qlora_int8_expert_bwd": (i32, [vp, vp, i64, i32, i64, i64, vp, vp, vp, vp, sz, vp]),
         "qlora_debug_fill": (i32, [vp, i64, ctypes.c_uint32, vp]),
         "qlora_debug_read": (i32, [vp, i64, ctypes.c_uint32, vp, vp]),
@@ -136,8 +136,10 @@ def _ptr(t):
 
 def _stream(stream=None):
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    # torch.cuda.current_stream().cuda_stream without building a Stream object (3.7 us a call)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _check(fn: str, st: int) -> None:
@@ -577,13 +579,13 @@ def alloc_int8_rows(shape, device) -> Int8Rows:
 def _need_int8_rows(name, r, dims):
     """Codes and scales of an Int8Rows hold exactly what its shape says."""
     torch = _torch()
-    if len(r.shape) != dims:
-        raise ValueError(f"{name} must be {dims}-D, got shape {tuple(r.shape)}")
-    lead, K = tuple(int(d) for d in r.shape[:-1]), int(r.shape[-1])
-    _need_shape(f"{name}.codes", r.codes, lead + (-(-K // 16) * 16,))
-    _need_shape(f"{name}.scale", r.scale, lead)
-    _need_dtype(torch.int8, **{f"{name}.codes": r.codes})
-    _need_dtype(torch.float32, **{f"{name}.scale": r.scale})
+    shape, codes, scale = tuple(r.shape), r.codes, r.scale
+    if len(shape) != dims:
+        raise ValueError(f"{name} must be {dims}-D, got shape {shape}")
+    if codes.shape != shape[:-1] + (-(-shape[-1] // 16) * 16,) or scale.shape != shape[:-1]:
+        raise ValueError(f"{name} of shape {shape} holds codes {tuple(codes.shape)} and scales {tuple(scale.shape)}")
+    if codes.dtype != torch.int8 or scale.dtype != torch.float32:
+        raise ValueError(f"{name} must hold int8 codes and float32 scales, got {codes.dtype} and {scale.dtype}")
 
 
 def qlora_int8_quantize_rows(x, out: Int8Rows | None = None, status=None, stream=None) -> Int8Rows:
@@ -629,74 +631,95 @@ def _int8_dims(rows, w, offsets, backward):
     """(T, E, N, K) of an Int8 call; offsets None: the dense linear, E = 1."""
     torch = _torch()
     _need_int8_rows("w", w, 2 if offsets is None else 3)
-    E = 1 if offsets is None else int(w.shape[0])
-    N, K = (int(d) for d in w.shape[-2:])
+    N, K = w.shape[-2:]
     name, width = ("dY", N) if backward else ("X", K)
     if isinstance(rows, Int8Rows):
         if backward:
             raise ValueError("dY must be a bfloat16 tensor")
         _need_int8_rows(name, rows, 2)
-    else:
-        if rows.dim() != 2:
-            raise ValueError(f"{name} must be 2-D")
-        _need_dtype(torch.bfloat16, **{name: rows})
-    if int(rows.shape[1]) != width:
-        raise ValueError(f"{name} has {rows.shape[1]} columns but the weight is {N} x {K}")
-    if offsets is not None:
-        _need_shape("offsets", offsets, (E + 1,))
-        _need_dtype(torch.int32, offsets=offsets)
-    return int(rows.shape[0]), E, N, K
+    elif rows.dtype != torch.bfloat16 or rows.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D bfloat16 tensor, got {rows.dim()}-D {rows.dtype}")
+    T, columns = rows.shape
+    if columns != width:
+        raise ValueError(f"{name} has {columns} columns but the weight is {N} x {K}")
+    if offsets is None:
+        return T, 1, N, K
+    E = w.shape[0]
+    if offsets.shape != (E + 1,) or offsets.dtype != torch.int32:
+        raise ValueError(f"offsets must be int32 [{E + 1}], got {offsets.dtype} {tuple(offsets.shape)}")
+    return T, E, N, K
+
+
+def _int8_buffers(out, shape, dtype, ws, need, like, stream):
+    """The output and the workspace (`need` bytes; none where that is 0), made
+    on `like`'s device where they are not given."""
+    if out is not None and (ws is not None or need == 0):
+        return out, ws
+    with _alloc_on(stream):
+        if out is None:
+            out = like.new_empty(shape, dtype=dtype)
+        if ws is None and need > 0:
+            ws = like.new_empty(need, dtype=_torch().uint8)
+    return out, ws
 
 
 def _int8_fwd(X, w, offsets, out_dtype, Y, ws, stream):
-    torch = _torch()
+    torch, lib = _torch(), _get_lib()
     T, E, N, K = _int8_dims(X, w, offsets, False)
-    quantized = isinstance(X, Int8Rows)
-    if Y is not None and out_dtype is None:
-        out_dtype = Y.dtype
-    out_dtype = out_dtype or torch.bfloat16
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if Y is None else Y.dtype
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
-    _need_shape("Y", Y, (T, N))
-    _need_dtype(out_dtype, Y=Y)
-    x_bufs = (X.codes, X.scale) if quantized else (X,)
-    _need_cuda(*x_bufs, w.codes, w.scale, offsets, Y, ws)
-    by_expert = offsets is not None
-    with _alloc_on(stream):
-        if Y is None:
-            Y = torch.empty((T, N), dtype=out_dtype, device=w.codes.device)
-        if ws is None:
-            need = (qlora_int8_expert_fwd_workspace_size(T, E, N, K) if by_expert
-                    else qlora_int8_linear_fwd_workspace_size(T, N, K))
-            ws = _workspace(need, w.codes.device)
-    fn = ("qlora_int8_expert_" if by_expert else "qlora_int8_") + \
-        ("matmul" if quantized else "fwd" if by_expert else "linear_fwd")
-    sizes = (_ptr(offsets), T, E, N, K) if by_expert else (T, N, K)
-    st = getattr(_get_lib(), fn)(*(_ptr(t) for t in x_bufs), *sizes, _ptr(w.codes), _ptr(w.scale), _ptr(Y),
-                                 0 if out_dtype == torch.float32 else 1, _ptr(ws), ws.numel(), _stream(stream))
-    _check(fn, st)
+    if Y is not None:
+        _need_shape("Y", Y, (T, N))
+        _need_dtype(out_dtype, Y=Y)
+    code = 0 if out_dtype == torch.float32 else 1
+    quantized = isinstance(X, Int8Rows)
+    if quantized:
+        _need_cuda(X.codes, X.scale, w.codes, w.scale, offsets, Y)
+        need = 0
+    else:
+        _need_cuda(X, w.codes, w.scale, offsets, Y, ws)
+        need = (lib.qlora_int8_linear_fwd_workspace_size(T, N, K) if offsets is None
+                else lib.qlora_int8_expert_fwd_workspace_size(T, E, N, K))
+    Y, ws = _int8_buffers(Y, (T, N), out_dtype, ws, need, w.scale, stream)
+    cs = _stream(stream)
+    scratch = (_ptr(ws), 0 if ws is None else ws.numel())
+    if offsets is None and quantized:
+        st = lib.qlora_int8_matmul(_ptr(X.codes), _ptr(X.scale), T, N, K, _ptr(w.codes), _ptr(w.scale), _ptr(Y), code,
+                                   cs)
+    elif offsets is None:
+        st = lib.qlora_int8_linear_fwd(_ptr(X), T, N, K, _ptr(w.codes), _ptr(w.scale), _ptr(Y), code, *scratch, cs)
+    elif quantized:
+        st = lib.qlora_int8_expert_matmul(_ptr(X.codes), _ptr(X.scale), _ptr(offsets), T, E, N, K, _ptr(w.codes),
+                                          _ptr(w.scale), _ptr(Y), code, cs)
+    else:
+        st = lib.qlora_int8_expert_fwd(_ptr(X), _ptr(offsets), T, E, N, K, _ptr(w.codes), _ptr(w.scale), _ptr(Y),
+                                       code, *scratch, cs)
+    if st != QLORA_OK:
+        _check("qlora_int8_linear_fwd" if offsets is None else "qlora_int8_expert_fwd", st)
     return Y
 
 
 def _int8_bwd(dY, w, offsets, dX, ws, stream):
-    torch = _torch()
+    torch, lib = _torch(), _get_lib()
     T, E, N, K = _int8_dims(dY, w, offsets, True)
-    _need_shape("dX", dX, (T, K))
-    _need_dtype(torch.bfloat16, dX=dX)
+    if dX is not None:
+        _need_shape("dX", dX, (T, K))
+        _need_dtype(torch.bfloat16, dX=dX)
     _need_cuda(dY, w.codes, w.scale, offsets, dX, ws)
-    by_expert = offsets is not None
-    with _alloc_on(stream):
-        if dX is None:
-            dX = torch.empty((T, K), dtype=torch.bfloat16, device=dY.device)
-        if ws is None:
-            need = (qlora_int8_expert_bwd_workspace_size(T, E, N, K) if by_expert
-                    else qlora_int8_linear_bwd_workspace_size(T, N, K))
-            ws = _workspace(need, dY.device)
-    fn = "qlora_int8_expert_bwd" if by_expert else "qlora_int8_linear_bwd"
-    sizes = (_ptr(offsets), T, E, N, K) if by_expert else (T, N, K)
-    st = getattr(_get_lib(), fn)(_ptr(dY), *sizes, _ptr(w.codes), _ptr(w.scale), _ptr(dX), _ptr(ws), ws.numel(),
-                                 _stream(stream))
-    _check(fn, st)
+    need = (lib.qlora_int8_linear_bwd_workspace_size(T, N, K) if offsets is None
+            else lib.qlora_int8_expert_bwd_workspace_size(T, E, N, K))
+    dX, ws = _int8_buffers(dX, (T, K), torch.bfloat16, ws, need, dY, stream)
+    cs = _stream(stream)
+    scratch = (_ptr(ws), 0 if ws is None else ws.numel())
+    if offsets is None:
+        st = lib.qlora_int8_linear_bwd(_ptr(dY), T, N, K, _ptr(w.codes), _ptr(w.scale), _ptr(dX), *scratch, cs)
+    else:
+        st = lib.qlora_int8_expert_bwd(_ptr(dY), _ptr(offsets), T, E, N, K, _ptr(w.codes), _ptr(w.scale), _ptr(dX),
+                                       *scratch, cs)
+    if st != QLORA_OK:
+        _check("qlora_int8_linear_bwd" if offsets is None else "qlora_int8_expert_bwd", st)
     return dX
 
 

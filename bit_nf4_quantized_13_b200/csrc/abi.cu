@@ -354,7 +354,8 @@ int qlora_device_error(int reset) {
     const int b = lora_device_error(reset);
     const int c = gemv_device_error(reset);
     const int d = int8_device_error(reset);
-    return a != QLORA_OK ? a : b != QLORA_OK ? b : c != QLORA_OK ? c : d;
+    const int e = int8_dx_device_error(reset);
+    return a != QLORA_OK ? a : b != QLORA_OK ? b : c != QLORA_OK ? c : d != QLORA_OK ? d : e;
 }
 
 int qlora_int8_quantize(const float* x, int64_t numel, int block, int8_t* codes, float* c, int32_t* status,
@@ -391,15 +392,18 @@ int check_int8(int64_t T, int E, int64_t N, int64_t K, bool by_expert, const int
     return QLORA_OK;
 }
 
-// Workspace of the forward: the tokens' codes, their scales, the product's.
+// Workspace of the forward: the tokens' codes and their scales (nothing where
+// the kernel quantizes them itself).
 size_t int8_codes_bytes(int64_t T, int64_t K) { return align256(static_cast<size_t>(T) * int8_row_bytes(K)); }
 size_t int8_fwd_ws(int64_t T, int E, int64_t N, int64_t K) {
     if (check_int8(T, E, N, K, false, nullptr) != QLORA_OK) return 0;
-    return int8_codes_bytes(T, K) + align256(static_cast<size_t>(T) * 4) + int8_pair_workspace(T);
+    const Int8Weight w{nullptr, nullptr, E, N, K, int8_row_bytes(K)};
+    if (T == 0 || int8_gemv_fused(T, w)) return 0;
+    return int8_codes_bytes(T, K) + align256(static_cast<size_t>(T) * 4);
 }
 size_t int8_bwd_ws(int64_t T, int E, int64_t N, int64_t K) {
     if (check_int8(T, E, N, K, false, nullptr) != QLORA_OK) return 0;
-    return 0;
+    return int8_dx_workspace(T, Int8Weight{nullptr, nullptr, E, N, K, int8_row_bytes(K)});
 }
 
 // X != nullptr: bf16 tokens, quantized into the workspace first; else
@@ -413,24 +417,25 @@ int int8_fwd(const uint16_t* X, const int8_t* x_codes, const float* x_scale, con
     if (!ok_ptr(w_codes) || !ok_ptr(w_scale)) return QLORA_ERR_INVALID_ARG;
     if (T == 0) return QLORA_OK;
     if (!ok_ptr(Y) || (quantized ? !ok_ptr(x_codes) || !ok_ptr(x_scale) : !ok_ptr(X))) return QLORA_ERR_INVALID_ARG;
-    if (!ws || !aligned16(ws) || ws_bytes < int8_fwd_ws(T, E, N, K)) return QLORA_ERR_WORKSPACE;
+    const size_t need = quantized ? 0 : int8_fwd_ws(T, E, N, K);
+    if (need > 0 && (!ws || !aligned16(ws) || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
     const Int8Weight w{w_codes, w_scale, E, N, K, int8_row_bytes(K)};
-    if (!int8_pair_supported(T, w)) return QLORA_ERR_UNSUPPORTED;
+    const RowRanges rr{offsets, T};
+    const bool few = int8_gemv_pays(T, w);
+    if (!few && !int8_pair_supported(T, w)) return QLORA_ERR_UNSUPPORTED;
     cudaStream_t cs = as_stream(stream);
-    int8_t* xc = static_cast<int8_t*>(ws);
-    float* xs = reinterpret_cast<float*>(xc + int8_codes_bytes(T, K));
-    int* gws = reinterpret_cast<int*>(reinterpret_cast<char*>(xs) + align256(static_cast<size_t>(T) * 4));
-    cudaError_t e;
-    if (quantized) {
-        e = cudaMemsetAsync(gws, 0, int8_pair_counter_bytes(), cs);
-    } else {
-        e = launch_int8_rows(X, 1, T, K, xc, xs, nullptr, cs, gws, static_cast<int>(int8_pair_counter_bytes() / 4));
+    if (!quantized && int8_gemv_fused(T, w))
+        return cuda_status(launch_int8_fwd_gemv(X, nullptr, nullptr, w, rr, Y, out_dtype, cs, false));
+    if (!quantized) {
+        int8_t* xc = static_cast<int8_t*>(ws);
+        float* xs = reinterpret_cast<float*>(xc + int8_codes_bytes(T, K));
+        const cudaError_t e = launch_int8_rows(X, 1, T, K, xc, xs, nullptr, cs);
+        if (e != cudaSuccess) return cuda_status(e);
         x_codes = xc;
         x_scale = xs;
     }
-    if (e == cudaSuccess)
-        e = launch_int8_fwd_pair(x_codes, x_scale, w, RowRanges{offsets, T}, Y, out_dtype, gws, cs, !quantized);
-    return pair_status(e);
+    if (few) return cuda_status(launch_int8_fwd_gemv(nullptr, x_codes, x_scale, w, rr, Y, out_dtype, cs, !quantized));
+    return pair_status(launch_int8_fwd_pair(x_codes, x_scale, w, rr, Y, out_dtype, cs, !quantized));
 }
 
 int int8_bwd(const uint16_t* dY, const int32_t* offsets, bool by_expert, int64_t T, int E, int64_t N, int64_t K,
@@ -440,9 +445,11 @@ int int8_bwd(const uint16_t* dY, const int32_t* offsets, bool by_expert, int64_t
     if (!ok_ptr(w_codes) || !ok_ptr(w_scale)) return QLORA_ERR_INVALID_ARG;
     if (T == 0) return QLORA_OK;
     if (!ok_ptr(dY) || !ok_ptr(dX)) return QLORA_ERR_INVALID_ARG;
-    if (!ws || !aligned16(ws) || ws_bytes < int8_bwd_ws(T, E, N, K)) return QLORA_ERR_WORKSPACE;
+    const size_t need = int8_bwd_ws(T, E, N, K);
+    if (need > 0 && (!ws || !aligned16(ws) || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
     const Int8Weight w{w_codes, w_scale, E, N, K, int8_row_bytes(K)};
-    return cuda_status(launch_int8_dx(dY, w, RowRanges{offsets, T}, dX, as_stream(stream)));
+    if (!int8_dx_supported(T, w)) return QLORA_ERR_UNSUPPORTED;
+    return pair_status(launch_int8_dx(dY, w, RowRanges{offsets, T}, dX, ws, as_stream(stream)));
 }
 
 }  // namespace
@@ -471,10 +478,9 @@ int qlora_int8_linear_fwd(const uint16_t* X, int64_t M, int64_t N, int64_t K, co
 }
 
 int qlora_int8_matmul(const int8_t* x_codes, const float* x_scale, int64_t M, int64_t N, int64_t K,
-                      const int8_t* w_codes, const float* w_scale, void* Y, int out_dtype, void* ws,
-                      size_t ws_bytes, void* stream) {
-    return int8_fwd(nullptr, x_codes, x_scale, nullptr, false, true, M, 1, N, K, w_codes, w_scale, Y, out_dtype, ws,
-                    ws_bytes, stream);
+                      const int8_t* w_codes, const float* w_scale, void* Y, int out_dtype, void* stream) {
+    return int8_fwd(nullptr, x_codes, x_scale, nullptr, false, true, M, 1, N, K, w_codes, w_scale, Y, out_dtype,
+                    nullptr, 0, stream);
 }
 
 int qlora_int8_linear_bwd(const uint16_t* dY, int64_t M, int64_t N, int64_t K, const int8_t* w_codes,
@@ -491,9 +497,9 @@ int qlora_int8_expert_fwd(const uint16_t* X, const int32_t* offsets, int64_t T, 
 
 int qlora_int8_expert_matmul(const int8_t* x_codes, const float* x_scale, const int32_t* offsets, int64_t T, int E,
                              int64_t N, int64_t K, const int8_t* w_codes, const float* w_scale, void* Y,
-                             int out_dtype, void* ws, size_t ws_bytes, void* stream) {
-    return int8_fwd(nullptr, x_codes, x_scale, offsets, true, true, T, E, N, K, w_codes, w_scale, Y, out_dtype, ws,
-                    ws_bytes, stream);
+                             int out_dtype, void* stream) {
+    return int8_fwd(nullptr, x_codes, x_scale, offsets, true, true, T, E, N, K, w_codes, w_scale, Y, out_dtype,
+                    nullptr, 0, stream);
 }
 
 int qlora_int8_expert_bwd(const uint16_t* dY, const int32_t* offsets, int64_t T, int E, int64_t N, int64_t K,

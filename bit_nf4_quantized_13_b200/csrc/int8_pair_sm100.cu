@@ -22,19 +22,14 @@
 // Two accumulators of 256 columns alternate, so a tile's epilogue runs under
 // the next tile's MMAs.
 //
-// Tiles go round-robin to the pairs.  When the last round would leave at
-// least half of the pairs idle (short batches, narrow weights), the stages of
-// its tiles are shared out evenly and a tile may be split along the
-// contraction: every part adds up in its own workspace slot, and the warp
-// that arrives last at a region's counter sums the slots.  No one waits for
-// another pair (two such kernels may share the GPU), and integer sums make
-// the result independent of the order.
+// Tiles go round-robin to the pairs.
 //
 // Every mbarrier wait is bounded; a timeout records QLORA_ERR_TIMEOUT in a
 // sticky device word and ends the role.
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "int8_tiles.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
 #include "tma_host.h"
@@ -48,7 +43,8 @@ namespace {
 using namespace sm100;
 
 constexpr int kRowsCta = 128;                  // output channels per CTA
-constexpr int kRowsPair = 2 * kRowsCta;        // MMA M
+constexpr int kRowsPair = kTileRows;           // MMA M: 128 in each CTA
+static_assert(kRowsPair == 2 * kRowsCta, "a tile's rows are halved between the CTAs");
 constexpr int kTileTok = 256;                  // largest MMA N
 constexpr int kBK = 128;                       // contraction bytes per stage
 constexpr int kStages = 6;
@@ -56,28 +52,28 @@ constexpr int kABytes = kRowsCta * kBK;        // 16 KiB
 constexpr int kBBytes = kTileTok / 2 * kBK;    // 16 KiB: half of the tokens in each CTA
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kEpiWarps = 8;
+constexpr int kWarpChunks = kTileTok / 32 / 2;   // 32-token chunks of an epilogue warp
 constexpr int kThreads = 32 * (2 + kEpiWarps);
-constexpr int kSmallBox = 16;                  // token rows of the ragged tiles' copies
 constexpr uint32_t kTmemCols = 512;
 constexpr int kBarOff = kStages * kStageBytes;
 constexpr int kTableOff = kBarOff + 256;
-constexpr int kSmemBytes = 1024 /* alignment slack */ + kTableOff + 2 * 4 * (QLORA_MAX_EXPERTS + 1);
+constexpr int kSmemBytes = 1024 /* alignment slack */ + kTableOff + kRowTableBytes;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 constexpr uint16_t kPairMask = 0x3;
-constexpr int kMinStagesPerPair = 4;
-constexpr int kCounters = 2 * kEpiWarps;       // regions of a tile: the epilogue warps of both CTAs
 
 struct Params {
     const float* xs;   // T token scales
     const float* ws;   // E x N channel scales
     RowRanges rr;
-    int E, N, K;
+    int E, N;
     int num_w;         // weight tiles of one expert
     int kbt;           // stages of a tile
     void* out;
-    int* counters;     // split tiles: kCounters per tail tile, zero at the start
-    int* partial;      // split tiles: two slots per pair
-    int slot_cols;     // tokens a slot holds (a multiple of 32)
+};
+
+struct Maps {
+    CUtensorMap w;          // weight rows: boxes of kRowsCta
+    CUtensorMap x[kBoxes];  // token rows: boxes of box_rows(i)
 };
 
 struct Pipe {
@@ -92,143 +88,36 @@ struct Pipe {
     __device__ uint32_t sB(int s) const { return sA(s) + kABytes; }
 };
 
-// The experts' row ranges and tiles, in shared memory.
-struct Table {
-    int* off;    // E + 1: expert e's rows are [off[e], off[e + 1]), ascending in [0, T]
-    int* tile0;  // E + 1: tiles of the experts before e; tile0[E]: all tiles
-};
-
-// A pair's share: `rounds` whole tiles pair + r * pairs, then (the first
-// `tpairs` pairs) the iterations [lo, hi) of the tail (tile * kbt + stage,
-// relative to tile `tail0`).  A range is at least kMinStagesPerPair and at
-// most half a tile (+ 1 stage) long, so it touches at most two tail tiles.
-struct Plan {
-    int pairs;    // pairs that take part
-    int rounds, tail0, tail_it, tpairs;
-    int lo, hi, t_first, nseg;
-};
-
-__device__ __forceinline__ int tail_lo(int pair, int tail_it, int tpairs) {
-    return static_cast<int>(static_cast<int64_t>(pair) * tail_it / tpairs);
-}
-
-__device__ __forceinline__ Plan make_plan(int units, int kbt, int pair, int num_pairs) {
-    Plan r{};
-    const int by_work = units * kbt / kMinStagesPerPair;  // < 2^31: checked by the host
-    r.pairs = max(1, min(num_pairs, by_work));
-    const int rem = units % r.pairs;
-    const int tpairs = min(r.pairs, rem * kbt / kMinStagesPerPair);
-    if (rem != 0 && 2 * rem <= tpairs) {
-        r.rounds = units / r.pairs;
-        r.tail0 = r.rounds * r.pairs;
-        r.tail_it = rem * kbt;
-        r.tpairs = tpairs;
-    } else {
-        r.rounds = pair < units ? (units - pair + r.pairs - 1) / r.pairs : 0;
-        r.tail0 = units;
-    }
-    if (pair >= r.pairs) {
-        r.rounds = 0;
-        return r;
-    }
-    if (pair < r.tpairs) {
-        r.lo = tail_lo(pair, r.tail_it, r.tpairs);
-        r.hi = tail_lo(pair + 1, r.tail_it, r.tpairs);
-        r.t_first = r.lo / kbt;
-    }
-    r.nseg = r.rounds + (r.hi > r.lo ? (r.hi - 1) / kbt - r.t_first + 1 : 0);
-    return r;
-}
-
-// One tile's part of the pair's work.
-struct Seg {
-    int expert, row0;          // expert, first output channel of the tile
-    int tok0, toks;            // first token row (of all T), tokens of the tile
-    int kb_begin, kb_end;
-    int tail_tile;             // split rounds: index of the tile in the tail, else -1
-};
-
-constexpr int kBand = 8;
-
-// Tile `unit`: experts in order; inside an expert bands of kBand weight
-// tiles with the token tiles slowest in a band, so the pairs at work at the
-// same time cover a compact block of tokens and channels (kept in L2).
-__device__ __forceinline__ void tile_of(const Params& p, const Table& tb, int unit, Seg& sg) {
-    int e = 0, above = p.E;  // tile0[e] <= unit < tile0[above]
-    while (above - e > 1) {
-        const int c = (e + above) >> 1;
-        if (tb.tile0[c] <= unit)
-            e = c;
-        else
-            above = c;
-    }
-    const int lo = tb.off[e], hi = tb.off[e + 1];
-    const int u = unit - tb.tile0[e];
-    const int num_t = (hi - lo + kTileTok - 1) / kTileTok;
-    const int band_tiles = kBand * num_t;
-    const int band = u / band_tiles, in = u % band_tiles;
-    const int rows_in_band = min(kBand, p.num_w - band * kBand);
-    const int t = in / rows_in_band;
-    sg.expert = e;
-    sg.row0 = (band * kBand + in % rows_in_band) * kRowsPair;
-    sg.tok0 = lo + t * kTileTok;
-    sg.toks = min(kTileTok, hi - sg.tok0);
-}
-
-__device__ __forceinline__ void seg_of(const Params& p, const Table& tb, const Plan& R, int pair, int i, Seg& sg) {
-    if (i < R.rounds) {
-        sg.kb_begin = 0;
-        sg.kb_end = p.kbt;
-        sg.tail_tile = -1;
-        tile_of(p, tb, pair + i * R.pairs, sg);
-    } else {
-        sg.tail_tile = R.t_first + (i - R.rounds);
-        const int base = sg.tail_tile * p.kbt;
-        sg.kb_begin = max(R.lo - base, 0);
-        sg.kb_end = min(R.hi - base, p.kbt);
-        tile_of(p, tb, R.tail0 + sg.tail_tile, sg);
-    }
-}
-
-__device__ __forceinline__ int mma_tokens(const Seg& sg) { return (sg.toks + 31) & ~31; }
-
-__device__ void role_tma(const Pipe& P, const Params& p, const Table& tb, const Plan& R, const CUtensorMap* tm_w,
-                         const CUtensorMap* tm_x, const CUtensorMap* tm_x16) {
+__device__ void role_tma(const Pipe& P, const Params& p, const RowTable& tb, int units, const Maps& maps) {
     int local = 0;
-    for (int i = 0; i < R.nseg; ++i) {
-        Seg sg;
-        seg_of(p, tb, R, P.pair, i, sg);
-        const int half = mma_tokens(sg) / 2;
-        const int wrow = sg.expert * p.N + sg.row0 + static_cast<int>(P.rank) * kRowsCta;
-        const int xrow = sg.tok0 + static_cast<int>(P.rank) * half;
-        const uint32_t tx = 2u * static_cast<uint32_t>(kABytes + half * kBK);
-        for (int kb = sg.kb_begin; kb < sg.kb_end; ++kb, ++local) {
+    for (int u = P.pair; u < units; u += P.num_pairs) {
+        const Tile tl = tile_of<kTileTok>(tb, p.E, p.num_w, u);
+        const int half = mma_tokens(tl.toks) / 2;
+        const int box = box_index(half);
+        const int wrow = tl.expert * p.N + tl.row0 + static_cast<int>(P.rank) * kRowsCta;
+        const int xrow = tl.tok0 + static_cast<int>(P.rank) * half;
+        const uint32_t tx = 2u * static_cast<uint32_t>(kABytes + box_rows(box) * kBK);
+        for (int kb = 0; kb < p.kbt; ++kb, ++local) {
             const int s = local % kStages;
             const uint32_t ph = static_cast<uint32_t>(local / kStages) & 1u;
             if (!mbar_wait(P.empty(s), ph ^ 1u, &g_int8_error)) return;
             const uint32_t bar = cluster_map(P.full(s), 0);
             if (P.rank == 0) mbar_arrive_expect_tx(P.full(s), tx);
-            tma_load_2d_pair(P.sA(s), tm_w, bar, kb * kBK, wrow);
-            if (half == kTileTok / 2) {
-                tma_load_2d_pair(P.sB(s), tm_x, bar, kb * kBK, xrow);
-            } else {
-                for (int r = 0; r < half; r += kSmallBox)
-                    tma_load_2d_pair(P.sB(s) + static_cast<uint32_t>(r * kBK), tm_x16, bar, kb * kBK, xrow + r);
-            }
+            tma_load_2d_pair(P.sA(s), &maps.w, bar, kb * kBK, wrow);
+            tma_load_2d_pair(P.sB(s), &maps.x[box], bar, kb * kBK, xrow);
         }
     }
 }
 
-__device__ void role_mma(const Pipe& P, const Params& p, const Table& tb, const Plan& R) {
-    int local = 0;
-    for (int i = 0; i < R.nseg; ++i) {
-        Seg sg;
-        seg_of(p, tb, R, P.pair, i, sg);
+__device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, int units) {
+    int local = 0, i = 0;
+    for (int u = P.pair; u < units; u += P.num_pairs, ++i) {
+        const Tile tl = tile_of<kTileTok>(tb, p.E, p.num_w, u);
         const int b = i & 1;
-        const uint32_t idesc = idesc_i8(kRowsPair, mma_tokens(sg));
+        const uint32_t idesc = idesc_i8(kRowsPair, mma_tokens(tl.toks));
         if (!mbar_wait(P.acc_empty(b), (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u, &g_int8_error)) return;
         tc_fence_after();
-        for (int kb = sg.kb_begin; kb < sg.kb_end; ++kb, ++local) {
+        for (int kb = 0; kb < p.kbt; ++kb, ++local) {
             const int s = local % kStages;
             const uint32_t ph = static_cast<uint32_t>(local / kStages) & 1u;
             if (!mbar_wait(P.full(s), ph, &g_int8_error)) return;
@@ -237,7 +126,7 @@ __device__ void role_mma(const Pipe& P, const Params& p, const Table& tb, const 
 #pragma unroll
             for (int kk = 0; kk < kBK / 32; ++kk)  // 32 bytes along a row: 2 descriptor units
                 mma_i8_ss_pair(P.tmem + b * kTileTok, ad + static_cast<uint64_t>(2 * kk),
-                               bd + static_cast<uint64_t>(2 * kk), idesc, (kb > sg.kb_begin || kk > 0) ? 1u : 0u);
+                               bd + static_cast<uint64_t>(2 * kk), idesc, (kb > 0 || kk > 0) ? 1u : 0u);
             tc_commit_pair_mc(P.empty(s), kPairMask);
         }
         tc_commit_pair_mc(P.acc_full(b), kPairMask);
@@ -252,163 +141,79 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int lan
     return ok != 0;
 }
 
-// Parts of tail tile t: the pairs whose ranges meet its kbt iterations.
-__device__ __forceinline__ int pair_of(const Plan& R, int it) {
-    return static_cast<int>((static_cast<int64_t>(it + 1) * R.tpairs - 1) / R.tail_it);
-}
-
-// Scales a chunk of 32 tokens (one column a token, one lane a channel),
-// rounds and stores it.  (RN32(sum) * sx) * sw, in that order: the first
-// product cannot leave the fp32 range for tokens whose scale is normal.
+// Scales a chunk of 32 tokens (a column each; a lane is a channel), rounds
+// and stores it: (RN32(sum) * sx) * sw, in that order, so that the first
+// product cannot leave the fp32 range for tokens whose scale is normal.  All
+// 32 values are formed before the first store: with a branch between them
+// each one exposed its own latency (60 cycles a token, 7 us a full tile).
 template <bool kF32>
-__device__ __forceinline__ void store_chunk(const Params& p, const uint32_t (&acc)[32], const Seg& sg, int col,
-                                            int chan, bool chan_ok, float sw, int lane) {
-    const int left = sg.toks - col;  // tokens of the chunk that exist
-    const float sx_lane = lane < left ? __ldg(p.xs + sg.tok0 + col + lane) : 0.0f;
-    const int64_t o = static_cast<int64_t>(sg.tok0 + col) * p.N + chan;
+__device__ __forceinline__ void store_chunk(const Params& p, const uint32_t (&acc)[32], const float* sx,
+                                            const Tile& tl, int col, int chan, float sw, int lane) {
+    const int left = tl.toks - col;  // tokens of the chunk that exist
+    float v[32];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const float sx = __shfl_sync(0xffffffffu, sx_lane, j);
-        const float v = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(acc[j])), sx), sw);
-        if (chan_ok && j < left) {
-            if (kF32)
-                static_cast<float*>(p.out)[o + static_cast<int64_t>(j) * p.N] = v;
-            else
-                static_cast<uint16_t*>(p.out)[o + static_cast<int64_t>(j) * p.N] = f32_to_bf16_bits(v);
-        }
+    for (int j4 = 0; j4 < 8; ++j4) {
+        const float4 s4 = *reinterpret_cast<const float4*>(sx + 4 * j4);
+        v[4 * j4] = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(acc[4 * j4])), s4.x), sw);
+        v[4 * j4 + 1] = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(acc[4 * j4 + 1])), s4.y), sw);
+        v[4 * j4 + 2] = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(acc[4 * j4 + 2])), s4.z), sw);
+        v[4 * j4 + 3] = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(acc[4 * j4 + 3])), s4.w), sw);
+    }
+    const int64_t row0 = static_cast<int64_t>(tl.tok0 + col) * p.N;
+    if constexpr (kF32) {
+        float* o = static_cast<float*>(p.out) + row0 + chan;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (chan < p.N && j < left) o[static_cast<int64_t>(j) * p.N] = v[j];
+    } else {
+        store_bf16_chunk(static_cast<uint16_t*>(p.out) + row0, p.N, chan, left, v, lane);
     }
 }
 
-__device__ __forceinline__ int4 ld_cg_i4(const int* p) {
-    int4 v;
-    asm volatile("ld.global.cg.v4.s32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
-                 : "memory");
-    return v;
-}
-
 template <bool kF32>
-__device__ void role_epilogue(const Pipe& P, const Params& p, const Table& tb, const Plan& R, int warp, int lane) {
+__device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb, int units, int warp, int lane) {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const int lrow = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const int64_t slot_ints = static_cast<int64_t>(kRowsPair) * p.slot_cols;
-    // this lane's 32 sums of column chunk c in slot `slot`: eight groups of
-    // four, one group 512 contiguous bytes a warp
-    auto slot_at = [&](int slot, int c, int g) {
-        return p.partial + slot * slot_ints + static_cast<int64_t>(P.rank) * (slot_ints / 2) +
-               (static_cast<int64_t>(c * 8 + g) * kRowsCta + lrow) * 4;
-    };
-    for (int i = 0; i < R.nseg; ++i) {
-        Seg sg;
-        seg_of(p, tb, R, P.pair, i, sg);
+    __shared__ __align__(16) float s_sx[kEpiWarps][kWarpChunks * 32];
+    float* sx = s_sx[warp - 2];
+    int i = 0;
+    for (int u = P.pair; u < units; u += P.num_pairs, ++i) {
+        const Tile tl = tile_of<kTileTok>(tb, p.E, p.num_w, u);
         const int b = i & 1;
-        const int chunks = mma_tokens(sg) / 32;
-        const bool whole = sg.kb_begin == 0 && sg.kb_end == p.kbt;
-        const int chan = sg.row0 + static_cast<int>(P.rank) * kRowsCta + lrow;
-        const bool chan_ok = chan < p.N;
-        const float sw = chan_ok ? __ldg(p.ws + static_cast<int64_t>(sg.expert) * p.N + chan) : 0.0f;
-        const int my_slot = whole ? 0 : 2 * P.pair + (sg.tail_tile - R.t_first);
+        const int chunks = mma_tokens(tl.toks) / 32;
+        const int chan = tl.row0 + static_cast<int>(P.rank) * kRowsCta + quarter * 32 + lane;
+        const float sw = chan < p.N ? __ldg(p.ws + static_cast<int64_t>(tl.expert) * p.N + chan) : 0.0f;
+        // the token scales of this warp's chunks, on their way before the sums are ready
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < kWarpChunks; ++q) {
+            const int tok = (half + 2 * q) * 32 + lane;
+            sx[q * 32 + lane] = tok < tl.toks ? p.xs[tl.tok0 + tok] : 0.0f;
+        }
+        __syncwarp();
         if (!warp_wait(P.acc_full(b), static_cast<uint32_t>(i >> 1) & 1u, lane)) return;
         tc_fence_after();
-#pragma unroll 1
+#pragma unroll 1  // the code of one chunk: a tile's first pass over it is fetched cold
         for (int c = half; c < chunks; c += 2) {
             uint32_t acc[32];
             tmem_ld_32x32b_x32(P.tmem + lane_base + static_cast<uint32_t>(b * kTileTok + c * 32), acc);
             tmem_wait_ld();
-            if (whole) {
-                store_chunk<kF32>(p, acc, sg, c * 32, chan, chan_ok, sw, lane);
-            } else {
-#pragma unroll
-                for (int g = 0; g < 8; ++g)
-                    *reinterpret_cast<int4*>(slot_at(my_slot, c, g)) =
-                        make_int4(static_cast<int>(acc[4 * g]), static_cast<int>(acc[4 * g + 1]),
-                                  static_cast<int>(acc[4 * g + 2]), static_cast<int>(acc[4 * g + 3]));
-            }
+            store_chunk<kF32>(p, acc, sx + (c / 2) * 32, tl, c * 32, chan, sw, lane);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(cluster_map(P.acc_empty(b), 0));
-        if (whole) continue;
-        // the region (this warp's channels and chunks) is complete once every
-        // part has counted itself; the last one to do so adds the slots
-        const int base = sg.tail_tile * p.kbt;
-        const int j0 = pair_of(R, base), j1 = pair_of(R, base + p.kbt - 1);
-        __threadfence();
-        __syncwarp();
-        int old = 0;
-        if (lane == 0)
-            old = atomicAdd(p.counters + sg.tail_tile * kCounters + static_cast<int>(P.rank) * kEpiWarps + (warp - 2), 1);
-        old = __shfl_sync(0xffffffffu, old, 0);
-        if (old != j1 - j0) continue;
-        __threadfence();
-#pragma unroll 1
-        for (int c = half; c < chunks; c += 2) {
-            uint32_t acc[32] = {};
-#pragma unroll 1
-            for (int j = j0; j <= j1; ++j) {
-                const int slot = 2 * j + (sg.tail_tile - tail_lo(j, R.tail_it, R.tpairs) / p.kbt);
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const int4 v = ld_cg_i4(slot_at(slot, c, g));
-                    acc[4 * g] += static_cast<uint32_t>(v.x);
-                    acc[4 * g + 1] += static_cast<uint32_t>(v.y);
-                    acc[4 * g + 2] += static_cast<uint32_t>(v.z);
-                    acc[4 * g + 3] += static_cast<uint32_t>(v.w);
-                }
-            }
-            store_chunk<kF32>(p, acc, sg, c * 32, chan, chan_ok, sw, lane);
-        }
-    }
-}
-
-// One warp.  An offset counts as no less than the one before it and at most
-// T, so the ranges are disjoint and inside the rows whatever it holds.
-__device__ __forceinline__ void build_table(const Params& p, const Table& tb, int lane) {
-    const int T = static_cast<int>(p.rr.T);
-    int top = 0, tiles = 0;  // the last offset and the tiles so far
-    if (lane == 0) {
-        top = p.rr.offsets ? min(max(p.rr.offsets[0], 0), T) : 0;
-        tb.off[0] = top;
-        tb.tile0[0] = 0;
-    }
-    top = __shfl_sync(0xffffffffu, top, 0);
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-        const int e = e0 + lane;
-        int hi = T;
-        if (p.rr.offsets) hi = e < p.E ? min(p.rr.offsets[e + 1], T) : 0;
-        hi = max(hi, top);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) hi = max(hi, __shfl_up_sync(0xffffffffu, hi, o));  // lanes < o: their own
-        int lo = __shfl_up_sync(0xffffffffu, hi, 1);
-        if (lane == 0) lo = top;
-        int n = e < p.E ? (hi - lo + kTileTok - 1) / kTileTok * p.num_w : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, n, o);
-            if (lane >= o) n += up;
-        }
-        if (e < p.E) {
-            tb.off[e + 1] = hi;
-            tb.tile0[e + 1] = tiles + n;
-        }
-        tiles += __shfl_sync(0xffffffffu, n, 31);
-        top = __shfl_sync(0xffffffffu, hi, 31);
     }
 }
 
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
-k_int8_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                 const __grid_constant__ CUtensorMap tm_x16, const __grid_constant__ Params p) {
+k_int8_gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
-    const Table tb{reinterpret_cast<int*>(smem + kTableOff),
-                   reinterpret_cast<int*>(smem + kTableOff) + QLORA_MAX_EXPERTS + 1};
-    __shared__ Plan s_plan;
+    const RowTable tb = row_table(smem + kTableOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     Pipe P;
@@ -434,29 +239,24 @@ k_int8_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
         tmem_relinquish_pair();
     }
     if (warp == 1 && lane == 0) {
-        tma_prefetch_desc(&tm_w);
-        tma_prefetch_desc(&tm_x);
-        tma_prefetch_desc(&tm_x16);
+        tma_prefetch_desc(&maps.w);
+        for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.x[i]);
     }
-    if (warp == 2) {
-        build_table(p, tb, lane);
-        __syncwarp();
-        if (lane == 0) s_plan = make_plan(tb.tile0[p.E], p.kbt, P.pair, P.num_pairs);
-    }
+    if (warp == 2) build_table<kTileTok>(p.rr, p.E, p.num_w, tb, lane);
     tc_fence_before();
     __syncthreads();
     cluster_arrive();  // both CTAs' barriers are initialised before any remote arrive
     cluster_wait();
     tc_fence_after();
     P.tmem = *tmem_slot;
-    const Plan& R = s_plan;
-    grid_dependency_wait();  // the quantized tokens, and the zeroed counters
+    const int units = tb.tile0[p.E];
+    grid_dependency_wait();  // the quantized tokens
     if (warp == 0) {
-        if (lane == 0) role_tma(P, p, tb, R, &tm_w, &tm_x, &tm_x16);
+        if (lane == 0) role_tma(P, p, tb, units, maps);
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0 && P.rank == 0) {
-            role_mma(P, p, tb, R);
+            role_mma(P, p, tb, units);
             // every pair MMA issued (also on an early exit) has completed
             // before the tensor memory can be freed
             tc_commit_pair_mc(P.drain(), 1);
@@ -464,7 +264,7 @@ k_int8_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
         }
         __syncwarp();
     } else {
-        role_epilogue<kF32>(P, p, tb, R, warp, lane);
+        role_epilogue<kF32>(P, p, tb, units, warp, lane);
     }
     tc_fence_before();
     __syncthreads();
@@ -528,24 +328,16 @@ int max_pairs() {
     return n;
 }
 
-int ws_pairs() { return num_sms() / 2 > 0 ? num_sms() / 2 : 1; }
-size_t counter_bytes() { return static_cast<size_t>(round_up(static_cast<int64_t>(ws_pairs()) * kCounters * 4, 256)); }
-int64_t slot_cols(int64_t T) { return T < kTileTok ? round_up(T, 32) : kTileTok; }
-
 template <bool kF32>
-cudaError_t launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const CUtensorMap& mx16, const Params& p,
-                        int64_t tiles, cudaStream_t st, bool dependent) {
+cudaError_t launch_pair(const Maps& maps, const Params& p, int64_t tiles, cudaStream_t st, bool dependent) {
     static ContextMemo<int> attr_memo;
     cudaError_t e = ensure_smem_limit(attr_memo, k_int8_gemm_pair<kF32>, kSmemBytes);
     if (e != cudaSuccess) return e;
-    int pairs = max_pairs<kF32>();
-    if (pairs > ws_pairs()) pairs = ws_pairs();
-    const int64_t by_work = tiles * p.kbt / kMinStagesPerPair;
-    if (by_work < pairs) pairs = static_cast<int>(by_work > 1 ? by_work : 1);
-    if (pairs <= 0) return cudaErrorNotSupported;
+    const int most = max_pairs<kF32>();
+    if (most <= 0) return cudaErrorNotSupported;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = pair_config(attr, pairs, st, dependent);
-    e = cudaLaunchKernelEx(&cfg, k_int8_gemm_pair<kF32>, mw, mx, mx16, p);
+    const cudaLaunchConfig_t cfg = pair_config(attr, static_cast<int>(tiles < most ? tiles : most), st, dependent);
+    e = cudaLaunchKernelEx(&cfg, k_int8_gemm_pair<kF32>, maps, p);
     note_launches(1);
     return e;
 }
@@ -553,45 +345,32 @@ cudaError_t launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const CUte
 }  // namespace
 
 // The largest number of tiles that T rows in E ranges can need.
-int64_t int8_pair_tiles(int64_t T, const Int8Weight& w) {
-    return (T / kTileTok + (T < w.E ? T : w.E)) * ceil_div(w.N, kRowsPair);
+int64_t int8_tiles(int64_t T, int E, int64_t w_rows, int tile_tok) {
+    return (T / tile_tok + (T < E ? T : E)) * ceil_div(w_rows, kTileRows);
 }
 
 bool int8_pair_supported(int64_t T, const Int8Weight& w) {
-    return int8_pair_tiles(T, w) * ceil_div(w.K, kBK) < (int64_t(1) << 31);
-}
-
-// Workspace: the counters (zeroed before every launch), then two slots per
-// pair of SMs.
-size_t int8_pair_counter_bytes() { return counter_bytes(); }
-size_t int8_pair_workspace(int64_t T) {
-    return counter_bytes() + static_cast<size_t>(ws_pairs()) * 2 * kRowsPair * static_cast<size_t>(slot_cols(T)) * 4;
+    return int8_tiles(T, w.E, w.N, kTileTok) * ceil_div(w.K, kBK) < (int64_t(1) << 31);
 }
 
 cudaError_t launch_int8_fwd_pair(const int8_t* x_codes, const float* x_scale, const Int8Weight& w,
-                                 const RowRanges& rr, void* out, int out_dtype, void* ws, cudaStream_t st,
-                                 bool dependent) {
+                                 const RowRanges& rr, void* out, int out_dtype, cudaStream_t st, bool dependent) {
     Params p{};
     p.xs = x_scale;
     p.ws = w.scale;
     p.rr = rr;
     p.E = w.E;
     p.N = static_cast<int>(w.N);
-    p.K = static_cast<int>(w.K);
     p.num_w = static_cast<int>(ceil_div(w.N, kRowsPair));
     p.kbt = static_cast<int>(ceil_div(w.K, kBK));
     p.out = out;
-    p.counters = static_cast<int*>(ws);
-    p.partial = reinterpret_cast<int*>(static_cast<char*>(ws) + counter_bytes());
-    p.slot_cols = static_cast<int>(slot_cols(rr.T));
-    CUtensorMap mw, mx, mx16;
-    if (!make_map_i8(&mw, w.codes, w.K, w.E * w.N, w.ld, kRowsCta) ||
-        !make_map_i8(&mx, x_codes, w.K, rr.T, w.ld, kTileTok / 2) ||
-        !make_map_i8(&mx16, x_codes, w.K, rr.T, w.ld, kSmallBox))
-        return cudaErrorInvalidValue;
-    const int64_t tiles = int8_pair_tiles(rr.T, w);
-    return out_dtype == 0 ? launch_pair<true>(mw, mx, mx16, p, tiles, st, dependent)
-                          : launch_pair<false>(mw, mx, mx16, p, tiles, st, dependent);
+    Maps maps;
+    bool ok = make_map_i8(&maps.w, w.codes, w.K, w.E * w.N, w.ld, kRowsCta);
+    for (int i = 0; i < kBoxes; ++i) ok = ok && make_map_i8(&maps.x[i], x_codes, w.K, rr.T, w.ld, box_rows(i));
+    if (!ok) return cudaErrorInvalidValue;
+    const int64_t tiles = int8_tiles(rr.T, w.E, w.N, kTileTok);
+    return out_dtype == 0 ? launch_pair<true>(maps, p, tiles, st, dependent)
+                          : launch_pair<false>(maps, p, tiles, st, dependent);
 }
 
 int int8_device_error(int reset) {

@@ -37,11 +37,10 @@ cudaError_t launch_int8_dequantize(const int8_t* codes, const float* c, int64_t 
 
 // int8_rows.cu -- Int8 absmax quantization of rows (eq. 1, one block per
 // row); x_dtype 0: fp32, 1: bf16.  Rows of codes are int8_row_bytes(K) apart.
-// Also zeroes n_zero ints at `zero` (the product's counters), and lets a
-// dependent launch start early.
+// Lets a dependent launch start early.
 __host__ __device__ inline int64_t int8_row_bytes(int64_t K) { return (K + 15) / 16 * 16; }
 cudaError_t launch_int8_rows(const void* x, int x_dtype, int64_t rows, int64_t K, int8_t* codes, float* scale,
-                             int32_t* status, cudaStream_t stream, int* zero = nullptr, int n_zero = 0);
+                             int32_t* status, cudaStream_t stream);
 
 // The frozen Int8 weight of one linear (E = 1) or of E experts: E x N rows of
 // K codes, ld = int8_row_bytes(K) bytes apart, with one scale each.
@@ -71,20 +70,29 @@ __device__ __forceinline__ void expert_rows(const RowRanges& rr, int e, int* lo,
 }
 
 // int8_pair_sm100.cu -- the forward on the tensor cores, on pairs of SMs
-// (out_dtype 0: fp32, 1: bf16).  The workspace's first
-// int8_pair_counter_bytes() must be zero when it starts; `dependent`: the
-// launch before it on the stream is the row quantizer, which it may overlap.
+// (out_dtype 0: fp32, 1: bf16).  `dependent`: the launch before it on the
+// stream is the row quantizer, which it may overlap.
+int64_t int8_tiles(int64_t T, int E, int64_t w_rows, int tile_tok);
 bool int8_pair_supported(int64_t T, const Int8Weight& w);
-size_t int8_pair_counter_bytes();
-size_t int8_pair_workspace(int64_t T);
 cudaError_t launch_int8_fwd_pair(const int8_t* x_codes, const float* x_scale, const Int8Weight& w,
-                                 const RowRanges& rr, void* out, int out_dtype, void* ws, cudaStream_t stream,
-                                 bool dependent);
+                                 const RowRanges& rr, void* out, int out_dtype, cudaStream_t stream, bool dependent);
 int int8_device_error(int reset);
 
-// int8_gemm.cu -- the input gradient
-cudaError_t launch_int8_dx(const uint16_t* dY, const Int8Weight& w, const RowRanges& rr, uint16_t* dX,
+// int8_gemv.cu -- the forward for a few tokens, by streaming the weights.
+// X != nullptr: bf16 tokens, quantized by the kernel itself
+// (int8_gemv_fused); else x_codes and x_scale.
+bool int8_gemv_pays(int64_t T, const Int8Weight& w);
+bool int8_gemv_fused(int64_t T, const Int8Weight& w);
+cudaError_t launch_int8_fwd_gemv(const uint16_t* X, const int8_t* x_codes, const float* x_scale, const Int8Weight& w,
+                                 const RowRanges& rr, void* out, int out_dtype, cudaStream_t stream, bool dependent);
+
+// int8_dx_sm100.cu -- the input gradient on the tensor cores, on pairs of SMs.
+// Workspace: dY's rows padded to 16 bytes, where N is not a multiple of 8.
+bool int8_dx_supported(int64_t T, const Int8Weight& w);
+size_t int8_dx_workspace(int64_t T, const Int8Weight& w);
+cudaError_t launch_int8_dx(const uint16_t* dY, const Int8Weight& w, const RowRanges& rr, uint16_t* dX, void* ws,
                            cudaStream_t stream);
+int int8_dx_device_error(int reset);
 
 // The frozen NF4 weight W (N x K row-major) as the GEMM kernels see it.
 struct Nf4Weight {

@@ -376,11 +376,10 @@ int qlora_int8_quantize_rows(const void* x, int x_dtype, int64_t rows, int64_t K
  * as written by qlora_int8_quantize_rows:
  *   Y[m][n] = out(RN32(RN32(RN32(sum_k x_codes[m][k] w_codes[n][k]) * x_scale[m]) * w_scale[n]))
  * The sum is exact (32-bit integers); out is fp32 (out_dtype 0) or bf16 bits
- * (out_dtype 1).  Y: M x N.  The workspace is that of qlora_int8_linear_fwd.
+ * (out_dtype 1).  Y: M x N.
  */
 int qlora_int8_matmul(const int8_t* x_codes, const float* x_scale, int64_t M, int64_t N, int64_t K,
-                      const int8_t* w_codes, const float* w_scale, void* Y, int out_dtype, void* ws,
-                      size_t ws_bytes, void* stream);
+                      const int8_t* w_codes, const float* w_scale, void* Y, int out_dtype, void* stream);
 
 /*
  * qlora_int8_linear_fwd -- the tokens X (M x K bf16) quantized by row, then
@@ -420,7 +419,7 @@ int qlora_int8_expert_fwd(const uint16_t* X, const int32_t* offsets, int64_t T, 
                           size_t ws_bytes, void* stream);
 int qlora_int8_expert_matmul(const int8_t* x_codes, const float* x_scale, const int32_t* offsets, int64_t T, int E,
                              int64_t N, int64_t K, const int8_t* w_codes, const float* w_scale, void* Y,
-                             int out_dtype, void* ws, size_t ws_bytes, void* stream);
+                             int out_dtype, void* stream);
 size_t qlora_int8_expert_bwd_workspace_size(int64_t T, int E, int64_t N, int64_t K);
 int qlora_int8_expert_bwd(const uint16_t* dY, const int32_t* offsets, int64_t T, int E, int64_t N, int64_t K,
                           const int8_t* w_codes, const float* w_scale, uint16_t* dX, void* ws, size_t ws_bytes,

@@ -37,41 +37,43 @@ def test_quantize_rows_refusals(lib):
 
 
 def test_linear_refusals(lib):
-    for f, x in ((lib.qlora_int8_linear_fwd, (P,)), (lib.qlora_int8_matmul, (P, P))):
-        assert f(*x, -1, 8, 8, P, P, P, 1, P, BIG, None) == INVALID
-        assert f(*x, 4, 0, 8, P, P, P, 1, P, BIG, None) == INVALID
-        assert f(*x, 4, 8, 0, P, P, P, 1, P, BIG, None) == INVALID
-        assert f(*x, 4, 8, 131073, P, P, P, 1, P, BIG, None) == UNSUPPORTED
-        assert f(*x, 1 << 30, 8, 8, P, P, P, 1, P, BIG, None) == UNSUPPORTED
-        assert f(*x, 4, 1 << 30, 8, P, P, P, 1, P, BIG, None) == UNSUPPORTED
-        assert f(*x, 4, 8, 8, P, P, P, 2, P, BIG, None) == INVALID   # unknown output type
-        assert f(*x, 4, 8, 8, P, P, P, -1, P, BIG, None) == INVALID
-        assert f(*x, 4, 8, 8, None, P, P, 1, P, BIG, None) == INVALID
-        assert f(*x, 4, 8, 8, P, P + 4, P, 1, P, BIG, None) == INVALID
-        assert f(*x, 4, 8, 8, P, P, None, 1, P, BIG, None) == INVALID
-        assert f(*(None,) * len(x), 4, 8, 8, P, P, P, 1, P, BIG, None) == INVALID
-        assert f(*x, 4, 8, 8, P, P, P, 1, None, BIG, None) == WORKSPACE
-        assert f(*x, 4, 8, 8, P, P, P, 1, P, 100, None) == WORKSPACE
-        assert f(*(None,) * len(x), 0, 8, 8, P, P, None, 1, None, 0, None) == OK  # no tokens
+    for f, x, ws in ((lib.qlora_int8_linear_fwd, (P,), (P, BIG)), (lib.qlora_int8_matmul, (P, P), ())):
+        assert f(*x, -1, 8, 8, P, P, P, 1, *ws, None) == INVALID
+        assert f(*x, 4, 0, 8, P, P, P, 1, *ws, None) == INVALID
+        assert f(*x, 4, 8, 0, P, P, P, 1, *ws, None) == INVALID
+        assert f(*x, 4, 8, 131073, P, P, P, 1, *ws, None) == UNSUPPORTED
+        assert f(*x, 1 << 30, 8, 8, P, P, P, 1, *ws, None) == UNSUPPORTED
+        assert f(*x, 4, 1 << 30, 8, P, P, P, 1, *ws, None) == UNSUPPORTED
+        assert f(*x, 4, 8, 8, P, P, P, 2, *ws, None) == INVALID   # unknown output type
+        assert f(*x, 4, 8, 8, P, P, P, -1, *ws, None) == INVALID
+        assert f(*x, 4, 8, 8, None, P, P, 1, *ws, None) == INVALID
+        assert f(*x, 4, 8, 8, P, P + 4, P, 1, *ws, None) == INVALID
+        assert f(*x, 4, 8, 8, P, P, None, 1, *ws, None) == INVALID
+        assert f(*(None,) * len(x), 4, 8, 8, P, P, P, 1, *ws, None) == INVALID
+        assert f(*(None,) * len(x), 0, 8, 8, P, P, None, 1, *((None, 0) if ws else ()), None) == OK  # no tokens
+    f = lib.qlora_int8_linear_fwd
+    assert f(P, 400, 8, 8, P, P, P, 1, None, BIG, None) == WORKSPACE
+    assert f(P, 400, 8, 8, P, P, P, 1, P + 8, BIG, None) == WORKSPACE
+    assert f(P, 400, 8, 8, P, P, P, 1, P, 100, None) == WORKSPACE
     f = lib.qlora_int8_linear_bwd
     assert f(P, -1, 8, 8, P, P, P, P, BIG, None) == INVALID
     assert f(P, 4, 8, 131073, P, P, P, P, BIG, None) == UNSUPPORTED
     assert f(None, 4, 8, 8, P, P, P, P, BIG, None) == INVALID
     assert f(P, 4, 8, 8, P, P, P + 2, P, BIG, None) == INVALID
     assert f(P, 4, 8, 8, None, P, P, P, BIG, None) == INVALID
-    assert f(P, 4, 8, 8, P, P, P, None, 0, None) == WORKSPACE
+    assert f(P, 400, 9, 8, P, P, P, None, 0, None) == WORKSPACE  # rows of dY to be padded
     assert f(None, 0, 8, 8, P, P, None, None, 0, None) == OK
 
 
 def test_expert_refusals(lib):
-    for f, x in ((lib.qlora_int8_expert_fwd, (P,)), (lib.qlora_int8_expert_matmul, (P, P))):
-        assert f(*x, P, 4, 0, 8, 8, P, P, P, 1, P, BIG, None) == INVALID
-        assert f(*x, P, 4, 1025, 8, 8, P, P, P, 1, P, BIG, None) == UNSUPPORTED
-        assert f(*x, P, 4, 1024, 1 << 22, 8, P, P, P, 1, P, BIG, None) == UNSUPPORTED  # E N >= 2^31
-        assert f(*x, None, 4, 2, 8, 8, P, P, P, 1, P, BIG, None) == INVALID            # no offsets
-        assert f(*x, P + 4, 4, 2, 8, 8, P, P, P, 1, P, BIG, None) == INVALID
-        assert f(*x, P, 4, 2, 8, 8, P, P, P, 1, P, 0, None) == WORKSPACE
-        assert f(*x, None, 0, 2, 8, 8, P, P, None, 1, None, 0, None) == OK
+    for f, x, ws in ((lib.qlora_int8_expert_fwd, (P,), (P, BIG)), (lib.qlora_int8_expert_matmul, (P, P), ())):
+        assert f(*x, P, 4, 0, 8, 8, P, P, P, 1, *ws, None) == INVALID
+        assert f(*x, P, 4, 1025, 8, 8, P, P, P, 1, *ws, None) == UNSUPPORTED
+        assert f(*x, P, 4, 1024, 1 << 22, 8, P, P, P, 1, *ws, None) == UNSUPPORTED  # E N >= 2^31
+        assert f(*x, None, 4, 2, 8, 8, P, P, P, 1, *ws, None) == INVALID            # no offsets
+        assert f(*x, P + 4, 4, 2, 8, 8, P, P, P, 1, *ws, None) == INVALID
+        assert f(*x, None, 0, 2, 8, 8, P, P, None, 1, *((None, 0) if ws else ()), None) == OK
+    assert lib.qlora_int8_expert_fwd(P, P, 400, 2, 8, 8, P, P, P, 1, P, 0, None) == WORKSPACE
     f = lib.qlora_int8_expert_bwd
     assert f(P, None, 4, 2, 8, 8, P, P, P, P, BIG, None) == INVALID
     assert f(P, P, 4, 1025, 8, 8, P, P, P, P, BIG, None) == UNSUPPORTED
@@ -85,6 +87,9 @@ def test_workspace_sizes(lib):
     assert q.qlora_int8_expert_fwd_workspace_size(100, 4, 8, 33) >= 100 * 48 + 400
     assert q.qlora_int8_linear_fwd_workspace_size(4, 8, 131073) == 0
     assert q.qlora_int8_expert_bwd_workspace_size(4, 1025, 8, 8) == 0
+    assert q.qlora_int8_linear_bwd_workspace_size(100, 64, 33) == 0
+    assert q.qlora_int8_linear_bwd_workspace_size(100, 33, 64) >= 100 * 40 * 2
+    assert q.qlora_int8_linear_fwd_workspace_size(1, 64, 4096) == 0  # one kernel that quantizes its own token
 
 
 def bf16(*shape):
