@@ -124,49 +124,50 @@ __device__ void role_tma(const Pipe& P, const Params& p, const RowTable& tb, int
     }
 }
 
-// Accumulators are taken in turn: the g-th one used is columns (g & 1) * 256,
-// for the (g >> 1)-th time.
-__device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, int units) {
-    int local = 0, g = 0;
-    for (int u = P.pair; u < units; u += P.num_pairs) {
-        const Tile tl = tile_of<kTileTok>(tb, p.w.E, p.num_w, u);
-        const int subs = tl.toks > kSubTok ? 2 : 1;
-        uint32_t idesc[kSubs];
-        for (int sub = 0; sub < subs; ++sub) {
-            idesc[sub] = idesc_bf16(kTileRows, mma_tokens(sub_tokens(tl, sub)), 1, 0);
-            const int a = g + sub;
-            if (!mbar_wait(P.acc_empty(a & 1), (static_cast<uint32_t>(a >> 1) & 1u) ^ 1u, &g_int8_dx_error)) return;
-        }
-        tc_fence_after();
-        for (int kb = 0; kb < p.kbt; ++kb, ++local) {
-            const int s = local % kStages;
-            const uint32_t ph = static_cast<uint32_t>(local / kStages) & 1u;
-            if (!mbar_wait(P.full_b(s), ph, &g_int8_dx_error)) return;
-            if (!mbar_wait(P.full_a(s), ph, &g_int8_dx_error)) return;
-            tc_fence_after();
-            const uint32_t sa = P.sA(s);
-#pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {
-                const uint64_t ad = sdesc_mnmajor_sw128(sa + kk * 2048, kPanelBytes);  // 16 rows of 128 bytes
-                const uint32_t more = (kb > 0 || kk > 0) ? 1u : 0u;
-                mma_bf16_ss_pair(P.tmem + (g & 1) * kSubTok, ad,
-                                 sdesc_kmajor_sw128(P.sB(s, 0)) + static_cast<uint64_t>(kk * 2), idesc[0], more);
-                if (subs == 2)
-                    mma_bf16_ss_pair(P.tmem + ((g + 1) & 1) * kSubTok, ad,
-                                     sdesc_kmajor_sw128(P.sB(s, 1)) + static_cast<uint64_t>(kk * 2), idesc[1], more);
-            }
-            tc_commit_pair_mc(P.empty(s), kPairMask);
-        }
-        for (int sub = 0; sub < subs; ++sub, ++g) tc_commit_pair_mc(P.acc_full(g & 1), kPairMask);
-    }
-}
-
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int lane) {
     int ok = 1;
     if (lane == 0) ok = mbar_wait(bar, parity, &g_int8_dx_error) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
     __syncwarp();
     return ok != 0;
+}
+
+// Accumulators are taken in turn: the g-th one used is columns (g & 1) * 256,
+// for the (g >> 1)-th time.
+__device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, int units) {
+    const uint64_t a0 = sdesc_mnmajor_sw128(P.sA(0), kPanelBytes), b0 = sdesc_kmajor_sw128(P.sB(0, 0));
+    int s = 0, g = 0;
+    uint32_t ph = 0;
+    for (int u = P.pair; u < units; u += P.num_pairs) {
+        const Tile tl = tile_of<kTileTok>(tb, p.w.E, p.num_w, u);
+        const int subs = tl.toks > kSubTok ? 2 : 1;
+        const uint32_t idesc0 = idesc_bf16(kTileRows, mma_tokens(sub_tokens(tl, 0)), 1, 0);
+        const uint32_t idesc1 = idesc_bf16(kTileRows, mma_tokens(sub_tokens(tl, 1)), 1, 0);
+        for (int a = g; a < g + subs; ++a)
+            if (!mbar_wait(P.acc_empty(a & 1), (static_cast<uint32_t>(a >> 1) & 1u) ^ 1u, &g_int8_dx_error)) return;
+        tc_fence_after();
+        const uint32_t d0 = P.tmem + (g & 1) * kSubTok, d1 = P.tmem + ((g + 1) & 1) * kSubTok;
+        for (int kb = 0; kb < p.kbt; ++kb) {
+            if (!mbar_wait(P.full_b(s), ph, &g_int8_dx_error)) return;
+            if (!mbar_wait(P.full_a(s), ph, &g_int8_dx_error)) return;
+            tc_fence_after();
+            const uint64_t off = static_cast<uint64_t>(s) * (kStageBytes / 16);
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk) {
+                const uint64_t ad = a0 + off + kk * (2048 / 16);  // 16 rows of 128 bytes
+                const uint64_t bd = b0 + off + kk * 2;            // 32 bytes along a row
+                const uint32_t more = (kb > 0 || kk > 0) ? 1u : 0u;
+                mma_bf16_ss_pair(d0, ad, bd, idesc0, more);
+                if (subs == 2) mma_bf16_ss_pair(d1, ad, bd + kBHalfBytes / 16, idesc1, more);
+            }
+            tc_commit_pair_mc(P.empty(s), kPairMask);
+            if (++s == kStages) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+        for (int sub = 0; sub < subs; ++sub, ++g) tc_commit_pair_mc(P.acc_full(g & 1), kPairMask);
+    }
 }
 
 __device__ __forceinline__ uint4 ldg_codes(const int8_t* p) {
@@ -353,10 +354,10 @@ k_int8_dx_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params
     P.tmem = *tmem_slot;
     const int units = tb.tile0[p.w.E];
     if (warp == 0) {
-        if (lane == 0) role_tma(P, p, tb, units, maps);
+        if (elect_one()) role_tma(P, p, tb, units, maps);
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && P.rank == 0) {
+        if (P.rank == 0 && elect_one()) {
             role_mma(P, p, tb, units);
             // every pair MMA issued (also on an early exit) has completed
             // before the tensor memory can be freed

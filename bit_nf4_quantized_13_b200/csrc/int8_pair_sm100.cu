@@ -109,36 +109,40 @@ __device__ void role_tma(const Pipe& P, const Params& p, const RowTable& tb, int
     }
 }
 
-__device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, int units) {
-    int local = 0, i = 0;
-    for (int u = P.pair; u < units; u += P.num_pairs, ++i) {
-        const Tile tl = tile_of<kTileTok>(tb, p.E, p.num_w, u);
-        const int b = i & 1;
-        const uint32_t idesc = idesc_i8(kRowsPair, mma_tokens(tl.toks));
-        if (!mbar_wait(P.acc_empty(b), (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u, &g_int8_error)) return;
-        tc_fence_after();
-        for (int kb = 0; kb < p.kbt; ++kb, ++local) {
-            const int s = local % kStages;
-            const uint32_t ph = static_cast<uint32_t>(local / kStages) & 1u;
-            if (!mbar_wait(P.full(s), ph, &g_int8_error)) return;
-            tc_fence_after();
-            const uint64_t ad = sdesc_kmajor_sw128(P.sA(s)), bd = sdesc_kmajor_sw128(P.sB(s));
-#pragma unroll
-            for (int kk = 0; kk < kBK / 32; ++kk)  // 32 bytes along a row: 2 descriptor units
-                mma_i8_ss_pair(P.tmem + b * kTileTok, ad + static_cast<uint64_t>(2 * kk),
-                               bd + static_cast<uint64_t>(2 * kk), idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-            tc_commit_pair_mc(P.empty(s), kPairMask);
-        }
-        tc_commit_pair_mc(P.acc_full(b), kPairMask);
-    }
-}
-
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int lane) {
     int ok = 1;
     if (lane == 0) ok = mbar_wait(bar, parity, &g_int8_error) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
     __syncwarp();
     return ok != 0;
+}
+
+__device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, int units) {
+    const uint64_t a0 = sdesc_kmajor_sw128(P.sA(0)), b0 = sdesc_kmajor_sw128(P.sB(0));
+    int s = 0, i = 0;
+    uint32_t ph = 0;
+    for (int u = P.pair; u < units; u += P.num_pairs, ++i) {
+        const Tile tl = tile_of<kTileTok>(tb, p.E, p.num_w, u);
+        const int b = i & 1;
+        const uint32_t idesc = idesc_i8(kRowsPair, mma_tokens(tl.toks));
+        if (!mbar_wait(P.acc_empty(b), (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u, &g_int8_error)) return;
+        tc_fence_after();
+        for (int kb = 0; kb < p.kbt; ++kb) {
+            if (!mbar_wait(P.full(s), ph, &g_int8_error)) return;
+            tc_fence_after();
+            const uint64_t off = static_cast<uint64_t>(s) * (kStageBytes / 16);
+#pragma unroll
+            for (int kk = 0; kk < kBK / 32; ++kk)  // 32 bytes along a row: 2 descriptor units
+                mma_i8_ss_pair(P.tmem + b * kTileTok, a0 + off + 2 * kk, b0 + off + 2 * kk, idesc,
+                                    (kb > 0 || kk > 0) ? 1u : 0u);
+            tc_commit_pair_mc(P.empty(s), kPairMask);
+            if (++s == kStages) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+        tc_commit_pair_mc(P.acc_full(b), kPairMask);
+    }
 }
 
 // Scales a chunk of 32 tokens (a column each; a lane is a channel), rounds
@@ -252,10 +256,10 @@ k_int8_gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Para
     const int units = tb.tile0[p.E];
     grid_dependency_wait();  // the quantized tokens
     if (warp == 0) {
-        if (lane == 0) role_tma(P, p, tb, units, maps);
+        if (elect_one()) role_tma(P, p, tb, units, maps);
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && P.rank == 0) {
+        if (P.rank == 0 && elect_one()) {
             role_mma(P, p, tb, units);
             // every pair MMA issued (also on an early exit) has completed
             // before the tensor memory can be freed

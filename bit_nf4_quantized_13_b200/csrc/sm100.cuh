@@ -45,6 +45,22 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
+// True in one lane of the (converged) warp.  The compiler knows that a region
+// guarded by it runs in one lane and keeps the operands of tensor-core
+// instructions in uniform registers: an MMA then issues at the tensor cores'
+// own rate (39, 43, 64 and 128 cycles for N = 32, 64, 128 and 256 of a pair),
+// where under `lane == 0` its operands are moved first (46 to 190 cycles each,
+// whatever N).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 r;\n\t"
+        "elect.sync r|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
 // Waits for the phase with the given parity to complete.  Gives up after
 // `limit_ns` of wall time, records QLORA_ERR_TIMEOUT in *err and returns
 // false, so a broken pipeline ends the kernel instead of hanging the GPU.
