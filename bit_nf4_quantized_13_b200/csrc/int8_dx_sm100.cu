@@ -124,12 +124,9 @@ __device__ void role_tma(const Pipe& P, const Params& p, const RowTable& tb, int
     }
 }
 
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int lane) {
-    int ok = 1;
-    if (lane == 0) ok = mbar_wait(bar, parity, &g_int8_dx_error) ? 1 : 0;
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    __syncwarp();
-    return ok != 0;
+// Every lane waits; the warp proceeds (or gives up) together.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, &g_int8_dx_error));
 }
 
 // Accumulators are taken in turn: the g-th one used is columns (g & 1) * 256,
@@ -179,15 +176,28 @@ __device__ __forceinline__ uint4 ldg_codes(const int8_t* p) {
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// Four codes -> two bf16 pairs of RN32(code * sc).
-__device__ __forceinline__ void convert4(uint32_t codes, float sc, uint32_t& lo, uint32_t& hi) {
+// Four codes -> two bf16 pairs of RN32(code * sc); ms = {sc, sc}.  The fp32
+// steps are done two at a time (each half is the ordinary IEEE operation).
+__device__ __forceinline__ void convert4(uint32_t codes, uint64_t ms, uint32_t& lo, uint32_t& hi) {
     const uint32_t u = codes ^ 0x80808080u;  // code + 128
-    float f[4];
+    uint32_t f[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        f[i] = __fmul_rn(__fadd_rn(__uint_as_float(prmt(u, 0x4B000000u, 0x7540u + i)), -8388736.0f), sc);
-    lo = pack_bf16x2(f[0], f[1]);
-    hi = pack_bf16x2(f[2], f[3]);
+    for (int i = 0; i < 4; ++i) f[i] = prmt(u, 0x4B000000u, 0x7540u + i);  // 2^23 + 128 + code
+    asm("{\n\t.reg .b64 a, b, m;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "mov.b64 m, {%7, %7};\n\t"
+        "add.rn.f32x2 a, a, m;\n\t"
+        "add.rn.f32x2 b, b, m;\n\t"
+        "mul.rn.f32x2 a, a, %6;\n\t"
+        "mul.rn.f32x2 b, b, %6;\n\t"
+        ".reg .f32 a0, a1, b0, b1;\n\t"
+        "mov.b64 {a0, a1}, a;\n\t"
+        "mov.b64 {b0, b1}, b;\n\t"
+        "cvt.rn.bf16x2.f32 %0, a1, a0;\n\t"
+        "cvt.rn.bf16x2.f32 %1, b1, b0;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3]), "l"(ms), "r"(0xCB000080u /* -(2^23 + 128) */));
 }
 
 // Outputs of the tile `tl`, whose accumulators are the g-th and following:
@@ -201,7 +211,7 @@ __device__ __forceinline__ bool tile_epilogue(const Pipe& P, const Params& p, co
     for (int sub = 0; sub < subs; ++sub, ++g) {
         const int b = g & 1;
         const int toks = sub_tokens(tl, sub);
-        if (!warp_wait(P.acc_full(b), static_cast<uint32_t>(g >> 1) & 1u, lane)) return false;
+        if (!warp_wait(P.acc_full(b), static_cast<uint32_t>(g >> 1) & 1u)) return false;
         tc_fence_after();
 #pragma unroll 1
         for (int c = part; c * 32 < toks; c += kParts) {
@@ -228,59 +238,69 @@ __device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb,
     const int r = lane >> 2, c = lane & 3;         // row within 8, 16-code piece of the 64
     const uint32_t full_a0 = cluster_map(P.full_a(part), 0);
     const int tiles = P.pair < units ? (units - P.pair + P.num_pairs - 1) / P.num_pairs : 0;
-    const int n_local = tiles * p.kbt;
     const int ld = static_cast<int>(p.w.ld), N = static_cast<int>(p.w.N);
     const uint32_t dst = P.sA(part) + static_cast<uint32_t>(panel * kPanelBytes);
 
-    // the tile whose codes are being loaded
-    int l_tile = -1;
-    const int8_t* l_codes = nullptr;  // row 0 of its expert, this lane's first column
+    // the cursor of the code loads: stage l_kb of this pair's tile l_tile
+    int l_tile = 0, l_kb = part;
+    const int8_t* l_codes = nullptr;  // row 0 of the tile's expert, this lane's first column
     const float* l_scale = nullptr;
     bool l_in = false;                // the column is inside the padded row
+    auto open_tile = [&]() {          // moves l_kb into its tile
+        while (l_kb >= p.kbt) {
+            l_kb -= p.kbt;
+            ++l_tile;
+        }
+        if (l_tile >= tiles) return;
+        const Tile tl = tile_of<kTileTok>(tb, p.w.E, p.num_w, P.pair + l_tile * P.num_pairs);
+        const int k = tl.row0 + static_cast<int>(P.rank) * kRowsCta + panel * 64 + c * 16;
+        l_codes = p.w.codes + static_cast<int64_t>(tl.expert) * N * ld + k;
+        l_scale = p.w.scale + static_cast<int64_t>(tl.expert) * N;
+        l_in = k < ld;
+    };
     uint4 cb[4];
     float sc[4];
-    auto issue = [&](int local) {
-        if (local >= n_local) return;
-        const int t = local / p.kbt, kb = local - t * p.kbt;
-        if (t != l_tile) {
-            l_tile = t;
-            const Tile tl = tile_of<kTileTok>(tb, p.w.E, p.num_w, P.pair + t * P.num_pairs);
-            const int k = tl.row0 + static_cast<int>(P.rank) * kRowsCta + panel * 64 + c * 16;
-            l_codes = p.w.codes + static_cast<int64_t>(tl.expert) * N * ld + k;
-            l_scale = p.w.scale + static_cast<int64_t>(tl.expert) * N;
-            l_in = k < ld;
-        }
-        const int n0 = kb * kBK + (quarter & 1) * 32 + r;
+    const int64_t ld8 = static_cast<int64_t>(8) * ld;
+    auto issue = [&]() {  // loads the cursor's stage and moves the cursor to this part's next one
+        if (l_tile >= tiles) return;
+        const int n0 = l_kb * kBK + (quarter & 1) * 32 + r;
         const int8_t* src = l_codes + static_cast<int64_t>(n0) * ld;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const bool ok = l_in && n0 + 8 * j < N;  // rows past N are zero (they are part of the contraction)
-            cb[j] = ok ? ldg_codes(src + static_cast<int64_t>(8 * j) * ld) : make_uint4(0u, 0u, 0u, 0u);
+            cb[j] = ok ? ldg_codes(src + j * ld8) : make_uint4(0u, 0u, 0u, 0u);
             sc[j] = ok ? __ldg(l_scale + n0 + 8 * j) : 0.0f;
         }
-        // this part's stage after the next one of the same tile, towards L2:
-        // the loads above cover only one stage's latency
-        if (c == 0 && l_in && kb + 2 * kStages < p.kbt) {
+        // this part's next stage but one of the same tile, towards L2: the
+        // loads above are only one of this part's stages ahead
+        if (c == 0 && l_in && l_kb + 2 * kStages < p.kbt) {
+            const int8_t* far = src + static_cast<int64_t>(2 * kStages * kBK) * ld;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (n0 + 2 * kStages * kBK + 8 * j < N)
-                    prefetch_l2(src + static_cast<int64_t>(2 * kStages * kBK + 8 * j) * ld);
+                if (n0 + 2 * kStages * kBK + 8 * j < N) prefetch_l2(far + j * ld8);
         }
+        l_kb += kStages;
+        if (l_kb >= p.kbt) open_tile();
     };
 
     int next_epi = 0, g = 0;  // the next tile whose outputs this warp writes
-    issue(part);
-    for (int local = part; local < n_local; local += kStages) {
-        const int t = local / p.kbt;
-        const uint32_t ph = static_cast<uint32_t>(local / kStages) & 1u;
+    open_tile();
+    issue();
+    uint32_t ph = 1;
+    int tile = 0, kb = part;  // the stage being converted
+    for (;; kb += kStages) {
+        for (; kb >= p.kbt; kb -= p.kbt) ++tile;
+        if (tile >= tiles) break;
         uint32_t v[32];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint32_t w4[4] = {cb[j].x, cb[j].y, cb[j].z, cb[j].w};
+            const uint64_t ms = (static_cast<uint64_t>(__float_as_uint(sc[j])) << 32) | __float_as_uint(sc[j]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) convert4(w4[i], sc[j], v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+            for (int i = 0; i < 4; ++i) convert4(w4[i], ms, v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
         }
-        if (!warp_wait(P.empty(part), ph ^ 1u, lane)) return;
+        if (!warp_wait(P.empty(part), ph)) return;
+        ph ^= 1u;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int row = (quarter & 1) * 32 + 8 * j + r;  // row & 7 == r
@@ -297,12 +317,12 @@ __device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb,
         if (lane == 0) mbar_arrive_remote(full_a0);
         // the tiles before this stage's are complete or about to be: write
         // them now, with the next tile's first stages already converted
-        while (next_epi < t) {
+        while (next_epi < tile) {
             const Tile tl = tile_of<kTileTok>(tb, p.w.E, p.num_w, P.pair + next_epi * P.num_pairs);
             if (!tile_epilogue(P, p, tl, g, part, quarter, lane)) return;
             ++next_epi;
         }
-        issue(local + kStages);
+        issue();
     }
     while (next_epi < tiles) {
         const Tile tl = tile_of<kTileTok>(tb, p.w.E, p.num_w, P.pair + next_epi * P.num_pairs);
