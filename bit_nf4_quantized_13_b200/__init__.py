@@ -25,7 +25,6 @@ Entry points (same names as the C ABI):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -150,18 +149,19 @@ def _check(fn: str, st: int) -> None:
 def _need_cuda(*ts):
     """Contiguous CUDA tensors, all on one device (the current one while the
     call runs: the library launches on the current device's stream)."""
-    dev = None
+    index = None
     for t in ts:
         if t is None:
             continue
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError("tensors must be contiguous CUDA tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    if dev is not None and dev.index is not None and dev.index != _torch().cuda.current_device():
-        raise ValueError(f"tensors are on {dev} but the current device is cuda:"
+        i = t.get_device()
+        if index is None:
+            index = i
+        elif i != index:
+            raise ValueError(f"tensors on different devices: cuda:{index} and cuda:{i}")
+    if index is not None and index != _torch().cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{index} but the current device is cuda:"
                          f"{_torch().cuda.current_device()}")
 
 
@@ -563,12 +563,6 @@ class Int8Rows:
         return sum(int(t.numel() * t.element_size()) for t in (self.codes, self.scale))
 
 
-def _alloc_on(stream):
-    """Buffers made inside belong to `stream` (None: the current one), so that
-    torch's allocator hands their memory on only in that stream's order."""
-    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
-
-
 def alloc_int8_rows(shape, device) -> Int8Rows:
     torch = _torch()
     shape = tuple(int(d) for d in shape)
@@ -596,8 +590,12 @@ def qlora_int8_quantize_rows(x, out: Int8Rows | None = None, status=None, stream
         raise ValueError(f"x must be float32 or bfloat16, got {x.dtype}")
     if x.dim() < 2 or int(x.shape[-1]) < 1:
         raise ValueError("x must have at least two dimensions and a non-empty last one")
-    with _alloc_on(stream):
-        r = out if out is not None else alloc_int8_rows(x.shape, x.device)
+    r = out
+    if r is None and stream is None:
+        r = alloc_int8_rows(x.shape, x.device)
+    elif r is None:  # the buffers belong to the call's stream
+        with torch.cuda.stream(stream):
+            r = alloc_int8_rows(x.shape, x.device)
     if tuple(r.shape) != tuple(x.shape):
         raise ValueError(f"out has shape {tuple(r.shape)}, x {tuple(x.shape)}")
     _need_int8_rows("out", r, x.dim())
@@ -652,14 +650,15 @@ def _int8_dims(rows, w, offsets, backward):
 
 def _int8_buffers(out, shape, dtype, ws, need, like, stream):
     """The output and the workspace (`need` bytes; none where that is 0), made
-    on `like`'s device where they are not given."""
-    if out is not None and (ws is not None or need == 0):
-        return out, ws
-    with _alloc_on(stream):
-        if out is None:
-            out = like.new_empty(shape, dtype=dtype)
-        if ws is None and need > 0:
-            ws = like.new_empty(need, dtype=_torch().uint8)
+    on `like`'s device where they are not given.  They belong to the call's
+    stream, so that torch's allocator hands their memory on in its order."""
+    if stream is not None and (out is None or (ws is None and need > 0)):
+        with _torch().cuda.stream(stream):
+            return _int8_buffers(out, shape, dtype, ws, need, like, None)
+    if out is None:
+        out = like.new_empty(shape, dtype=dtype)
+    if ws is None and need > 0:
+        ws = like.new_empty(need, dtype=_torch().uint8)
     return out, ws
 
 
@@ -675,29 +674,31 @@ def _int8_fwd(X, w, offsets, out_dtype, Y, ws, stream):
         _need_dtype(out_dtype, Y=Y)
     code = 0 if out_dtype == torch.float32 else 1
     quantized = isinstance(X, Int8Rows)
+    wc, wsc = w.codes, w.scale
+    # addresses go as plain integers: a ctypes object for each costs more than the check of a call
     if quantized:
-        _need_cuda(X.codes, X.scale, w.codes, w.scale, offsets, Y)
-        need = 0
+        _need_cuda(X.codes, X.scale, wc, wsc, offsets, Y)
+        Y, _ = _int8_buffers(Y, (T, N), out_dtype, None, 0, wsc, stream)
+        tail = (wc.data_ptr(), wsc.data_ptr(), Y.data_ptr(), code, _stream(stream))
+        if offsets is None:
+            fn, st = "qlora_int8_matmul", lib.qlora_int8_matmul(X.codes.data_ptr(), X.scale.data_ptr(), T, N, K, *tail)
+        else:
+            fn, st = "qlora_int8_expert_matmul", lib.qlora_int8_expert_matmul(
+                X.codes.data_ptr(), X.scale.data_ptr(), offsets.data_ptr(), T, E, N, K, *tail)
     else:
-        _need_cuda(X, w.codes, w.scale, offsets, Y, ws)
+        _need_cuda(X, wc, wsc, offsets, Y, ws)
         need = (lib.qlora_int8_linear_fwd_workspace_size(T, N, K) if offsets is None
                 else lib.qlora_int8_expert_fwd_workspace_size(T, E, N, K))
-    Y, ws = _int8_buffers(Y, (T, N), out_dtype, ws, need, w.scale, stream)
-    cs = _stream(stream)
-    scratch = (_ptr(ws), 0 if ws is None else ws.numel())
-    if offsets is None and quantized:
-        st = lib.qlora_int8_matmul(_ptr(X.codes), _ptr(X.scale), T, N, K, _ptr(w.codes), _ptr(w.scale), _ptr(Y), code,
-                                   cs)
-    elif offsets is None:
-        st = lib.qlora_int8_linear_fwd(_ptr(X), T, N, K, _ptr(w.codes), _ptr(w.scale), _ptr(Y), code, *scratch, cs)
-    elif quantized:
-        st = lib.qlora_int8_expert_matmul(_ptr(X.codes), _ptr(X.scale), _ptr(offsets), T, E, N, K, _ptr(w.codes),
-                                          _ptr(w.scale), _ptr(Y), code, cs)
-    else:
-        st = lib.qlora_int8_expert_fwd(_ptr(X), _ptr(offsets), T, E, N, K, _ptr(w.codes), _ptr(w.scale), _ptr(Y),
-                                       code, *scratch, cs)
+        Y, ws = _int8_buffers(Y, (T, N), out_dtype, ws, need, wsc, stream)
+        tail = (wc.data_ptr(), wsc.data_ptr(), Y.data_ptr(), code, None if ws is None else ws.data_ptr(),
+                0 if ws is None else ws.numel(), _stream(stream))
+        if offsets is None:
+            fn, st = "qlora_int8_linear_fwd", lib.qlora_int8_linear_fwd(X.data_ptr(), T, N, K, *tail)
+        else:
+            fn, st = "qlora_int8_expert_fwd", lib.qlora_int8_expert_fwd(X.data_ptr(), offsets.data_ptr(), T, E, N, K,
+                                                                        *tail)
     if st != QLORA_OK:
-        _check("qlora_int8_linear_fwd" if offsets is None else "qlora_int8_expert_fwd", st)
+        _check(fn, st)
     return Y
 
 
@@ -711,15 +712,15 @@ def _int8_bwd(dY, w, offsets, dX, ws, stream):
     need = (lib.qlora_int8_linear_bwd_workspace_size(T, N, K) if offsets is None
             else lib.qlora_int8_expert_bwd_workspace_size(T, E, N, K))
     dX, ws = _int8_buffers(dX, (T, K), torch.bfloat16, ws, need, dY, stream)
-    cs = _stream(stream)
-    scratch = (_ptr(ws), 0 if ws is None else ws.numel())
+    tail = (w.codes.data_ptr(), w.scale.data_ptr(), dX.data_ptr(), None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel(), _stream(stream))
     if offsets is None:
-        st = lib.qlora_int8_linear_bwd(_ptr(dY), T, N, K, _ptr(w.codes), _ptr(w.scale), _ptr(dX), *scratch, cs)
+        fn, st = "qlora_int8_linear_bwd", lib.qlora_int8_linear_bwd(dY.data_ptr(), T, N, K, *tail)
     else:
-        st = lib.qlora_int8_expert_bwd(_ptr(dY), _ptr(offsets), T, E, N, K, _ptr(w.codes), _ptr(w.scale), _ptr(dX),
-                                       *scratch, cs)
+        fn, st = "qlora_int8_expert_bwd", lib.qlora_int8_expert_bwd(dY.data_ptr(), offsets.data_ptr(), T, E, N, K,
+                                                                    *tail)
     if st != QLORA_OK:
-        _check("qlora_int8_linear_bwd" if offsets is None else "qlora_int8_expert_bwd", st)
+        _check(fn, st)
     return dX
 
 
