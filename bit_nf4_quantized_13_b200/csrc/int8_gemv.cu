@@ -13,9 +13,13 @@
 // consecutive codes of channels g and g + 8, which are the A fragments of two
 // mma.m16n8k32 (the contraction index is permuted the same way in both
 // operands, so no code moves between lanes); a warp reads 64 bytes of each of
-// 16 rows per instruction and keeps two halves of four such loads in flight.
-// Integer sums are exact, so the warps' partial sums may be added in any
-// order: through shared memory, once per 16 channels.
+// 16 rows per two instructions and keeps two halves of four such loads in
+// flight, across steps too.  Integer sums are exact, so the warps' partial
+// sums may be added in any order: through shared memory, once a step.  Two
+// blocks an SM (117 registers, no spills) stream as fast as three or four and
+// leave room for the token fragments; giving each warp whole steps, to have
+// fewer barriers, was slower (16 tokens, six experts of 11008 x 4096: 62
+// against 57 us).
 #include "int8_rows.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
@@ -29,9 +33,14 @@ constexpr int kRows = 16;               // output channels of a block's step
 constexpr int kUnit = 256;              // codes of a row in a warp's unit
 constexpr int kHalf = kUnit / 2;
 constexpr int kXPad = 64;               // bytes between token rows in shared memory, against bank conflicts
-constexpr int kMaxXSmem = 40 * 1024;
+constexpr int kBlocksPerSm = 2;
+// Tokens that every block quantizes itself: their bf16 values and their codes
+// stay in shared memory.  One kernel then does what two would, which saves 3
+// us on the host; its blocks repeat the work, which is why it ends here (5120
+// values: 1 us of the kernel).
+constexpr int kMaxFusedValues = 10240;
 constexpr int kMaxFused = 4;
-constexpr int kMaxTokens = 32;
+constexpr int kMaxTokens = 16;
 
 struct GemvParams {
     const uint16_t* X;   // fused: T x K bf16
@@ -64,9 +73,24 @@ struct HalfUnit {
     uint4 v[4];
 };
 
+// Eight values of token m from element e on.
+__device__ __forceinline__ RowVec<uint16_t, true> load_token(const GemvParams& p, int m, int e) {
+    const uint16_t* row = p.X + static_cast<int64_t>(m) * p.w.K;
+    RowVec<uint16_t, true> v;
+    if (p.w.K % 8 == 0) {
+        v.load(row, e, p.w.K);
+    } else {
+        RowVec<uint16_t, false> u;
+        u.load(row, e, p.w.K);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v.w[i] = u.w[i];
+    }
+    return v;
+}
+
 // NT tiles of 8 tokens at a time.
 template <int NT, bool kFused, bool kF32>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 k_int8_gemv(const GemvParams p) {
     extern __shared__ __align__(16) int8_t s_x[];  // fused: T rows of ld + kXPad bytes
     __shared__ int s_sum[kWarps][kRows][8 * NT];
@@ -77,6 +101,21 @@ k_int8_gemv(const GemvParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int ld = static_cast<int>(p.w.ld);  // T * ld < 2^31: checked by the host
     const int T = static_cast<int>(p.rr.T);
+
+    uint16_t* s_raw = reinterpret_cast<uint16_t*>(s_x + (kFused ? T * (ld + kXPad) : 0));  // fused: T rows of ld values
+    if (kFused) {
+        // the tokens' values first, before the weights' loads fill the memory system
+        for (int m = 0; m < T; ++m) {
+            uint32_t a = 0u;
+            for (int e = static_cast<int>(threadIdx.x) * 8; e < ld; e += kThreads * 8) {
+                const RowVec<uint16_t, true> v = load_token(p, m, e);
+                *reinterpret_cast<uint4*>(s_raw + m * ld + e) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+                a = abs_max(v, a);
+            }
+            a = __reduce_max_sync(0xffffffffu, a);
+            if (lane == 0) s_max[m][warp] = a;
+        }
+    }
 
     // the experts that have tokens, in order
     const bool dense = p.rr.offsets == nullptr;
@@ -138,26 +177,7 @@ k_int8_gemv(const GemvParams p) {
         advance();
     }
 
-    if (kFused) {  // quantize the T (<= kMaxFused) tokens
-        using V = RowVec<uint16_t, false>;
-        using VA = RowVec<uint16_t, true>;
-        const bool aligned = p.w.K % 8 == 0;
-        for (int m = 0; m < T; ++m) {
-            uint32_t a = 0u;
-            for (int e = static_cast<int>(threadIdx.x) * 8; e < ld; e += kThreads * 8) {
-                if (aligned) {
-                    VA v;
-                    v.load(p.X + m * p.w.K, e, p.w.K);
-                    a = abs_max(v, a);
-                } else {
-                    V v;
-                    v.load(p.X + m * p.w.K, e, p.w.K);
-                    a = abs_max(v, a);
-                }
-            }
-            a = __reduce_max_sync(0xffffffffu, a);
-            if (lane == 0) s_max[m][warp] = a;
-        }
+    if (kFused) {  // quantize them; a thread encodes the values that it staged
         __syncthreads();
         for (int m = 0; m < T; ++m) {
             uint32_t a = 0u;
@@ -166,17 +186,14 @@ k_int8_gemv(const GemvParams p) {
             float sc;
             const float c = row_constant(a, &sc);
             if (threadIdx.x == 0) s_scale[m] = sc;
-            int8_t* dst = s_x + m * (ld + kXPad);
             for (int e = static_cast<int>(threadIdx.x) * 8; e < ld; e += kThreads * 8) {
-                if (aligned) {
-                    VA v;
-                    v.load(p.X + m * p.w.K, e, p.w.K);
-                    encode(v, c, dst + e);
-                } else {
-                    V v;
-                    v.load(p.X + m * p.w.K, e, p.w.K);
-                    encode(v, c, dst + e);
-                }
+                const uint4 w = *reinterpret_cast<const uint4*>(s_raw + m * ld + e);
+                RowVec<uint16_t, true> v;
+                v.w[0] = w.x;
+                v.w[1] = w.y;
+                v.w[2] = w.z;
+                v.w[3] = w.w;
+                encode(v, c, s_x + m * (ld + kXPad) + e);
             }
         }
         __syncthreads();
@@ -255,14 +272,14 @@ k_int8_gemv(const GemvParams p) {
 template <int NT, bool kFused>
 cudaError_t gemv_launch(const GemvParams& p, int out_dtype, cudaStream_t st, bool dependent) {
     const int64_t steps = static_cast<int64_t>(p.groups) * (p.rr.T < p.w.E ? p.rr.T : p.w.E);
-    const int64_t cap = static_cast<int64_t>(num_sms()) * 3;
+    const int64_t cap = static_cast<int64_t>(num_sms()) * kBlocksPerSm;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(steps < cap ? steps : cap));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kFused ? static_cast<size_t>(p.rr.T) * (p.w.ld + kXPad) : 0;
+    cfg.dynamicSmemBytes = kFused ? static_cast<size_t>(p.rr.T) * (3 * p.w.ld + kXPad) : 0;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = dependent ? 1 : 0;
@@ -274,19 +291,22 @@ cudaError_t gemv_launch(const GemvParams& p, int out_dtype, cudaStream_t st, boo
 
 }  // namespace
 
-bool int8_gemv_pays(int64_t T, const Int8Weight& w) { return T <= kMaxTokens; }
-
-bool int8_gemv_fused(int64_t T, const Int8Weight& w) {
-    return T <= kMaxFused && T * (w.ld + kXPad) <= kMaxXSmem;
+// Up to 8 tokens always.  Up to 16, unless the tensor-core kernel's tiles (256
+// channels each) fill half of the SM pairs: 16 x 13824 x 5120 takes 24.6 us
+// here and 20.5 there, 16 x 4096 x 4096 12.3 and 16.4.
+bool int8_gemv_pays(int64_t T, const Int8Weight& w) {
+    if (T <= 8) return true;
+    return T <= kMaxTokens && int8_tiles(T, w.E, w.N, 256) * 4 < num_sms();
 }
+
+bool int8_gemv_fused(int64_t T, const Int8Weight& w) { return T <= kMaxFused && T * w.ld <= kMaxFusedValues; }
 
 cudaError_t launch_int8_fwd_gemv(const uint16_t* X, const int8_t* x_codes, const float* x_scale, const Int8Weight& w,
                                  const RowRanges& rr, void* out, int out_dtype, cudaStream_t st, bool dependent) {
     const GemvParams p{X, x_codes, x_scale, w, rr, static_cast<int>(ceil_div(w.N, kRows)), out};
     if (X) return gemv_launch<1, true>(p, out_dtype, st, false);
     if (rr.T <= 8) return gemv_launch<1, false>(p, out_dtype, st, dependent);
-    if (rr.T <= 16) return gemv_launch<2, false>(p, out_dtype, st, dependent);
-    return gemv_launch<4, false>(p, out_dtype, st, dependent);
+    return gemv_launch<2, false>(p, out_dtype, st, dependent);
 }
 
 }  // namespace qlora
