@@ -74,17 +74,13 @@ struct HalfUnit {
 };
 
 // Eight values of token m from element e on.
-__device__ __forceinline__ RowVec<uint16_t, true> load_token(const GemvParams& p, int m, int e) {
+__device__ __forceinline__ RowVec<uint16_t> load_token(const GemvParams& p, int m, int e) {
     const uint16_t* row = p.X + static_cast<int64_t>(m) * p.w.K;
-    RowVec<uint16_t, true> v;
-    if (p.w.K % 8 == 0) {
-        v.load(row, e, p.w.K);
-    } else {
-        RowVec<uint16_t, false> u;
-        u.load(row, e, p.w.K);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v.w[i] = u.w[i];
-    }
+    RowVec<uint16_t> v;
+    if (p.w.K % 8 == 0)
+        v.load<true>(row, e, p.w.K, nullptr);
+    else
+        v.load<false>(row, e, p.w.K, p.X + p.rr.T * p.w.K);
     return v;
 }
 
@@ -108,7 +104,7 @@ k_int8_gemv(const GemvParams p) {
         for (int m = 0; m < T; ++m) {
             uint32_t a = 0u;
             for (int e = static_cast<int>(threadIdx.x) * 8; e < ld; e += kThreads * 8) {
-                const RowVec<uint16_t, true> v = load_token(p, m, e);
+                const RowVec<uint16_t> v = load_token(p, m, e);
                 *reinterpret_cast<uint4*>(s_raw + m * ld + e) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
                 a = abs_max(v, a);
             }
@@ -188,7 +184,7 @@ k_int8_gemv(const GemvParams p) {
             if (threadIdx.x == 0) s_scale[m] = sc;
             for (int e = static_cast<int>(threadIdx.x) * 8; e < ld; e += kThreads * 8) {
                 const uint4 w = *reinterpret_cast<const uint4*>(s_raw + m * ld + e);
-                RowVec<uint16_t, true> v;
+                RowVec<uint16_t> v;
                 v.w[0] = w.x;
                 v.w[1] = w.y;
                 v.w[2] = w.z;

@@ -50,6 +50,7 @@ def compute_weight(w, e=None):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("rows,K", [(1, 1), (1, 5120), (3, 15), (5, 16), (2, 17), (9, 1024), (8, 1025), (7, 2048),
                                     (1000, 333), (4, 2049), (3, 8192), (3, 8200), (2, 16385), (2, 40000),
+                                    (257, 127), (333, 510), (65, 2047), (33, 4094), (33, 4099), (17, 8001),
                                     (4096, 512)])
 def test_rows_match_the_definition(rows, K, dtype):
     x = (torch.randn((rows, K), generator=gen(rows + K), device="cuda") * 3).to(dtype)
