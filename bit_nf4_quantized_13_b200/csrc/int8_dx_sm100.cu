@@ -71,6 +71,7 @@ struct Params {
     RowRanges rr;
     int num_w;      // column tiles: ceil(K / 256)
     int kbt;        // stages of a tile: ceil(N / 64)
+    int cap;        // most tokens of a tile: kTileTok or kSubTok
     uint16_t* dX;
 };
 
@@ -99,7 +100,7 @@ __device__ __forceinline__ int sub_tokens(const Tile& tl, int sub) {
 __device__ void role_tma(const Pipe& P, const Params& p, const RowTable& tb, int units, const Maps& maps) {
     int local = 0;
     for (int u = P.pair; u < units; u += P.num_pairs) {
-        const Tile tl = tile_of<kTileTok>(tb, p.w.E, p.num_w, u);
+        const Tile tl = tile_of(tb, p.w.E, p.num_w, p.cap, u);
         int box[kSubs], row[kSubs];
         uint32_t tx = 0;
         int subs = 0;
@@ -136,7 +137,7 @@ __device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, int
     int s = 0, g = 0;
     uint32_t ph = 0;
     for (int u = P.pair; u < units; u += P.num_pairs) {
-        const Tile tl = tile_of<kTileTok>(tb, p.w.E, p.num_w, u);
+        const Tile tl = tile_of(tb, p.w.E, p.num_w, p.cap, u);
         const int subs = tl.toks > kSubTok ? 2 : 1;
         const uint32_t idesc0 = idesc_bf16(kTileRows, mma_tokens(sub_tokens(tl, 0)), 1, 0);
         const uint32_t idesc1 = idesc_bf16(kTileRows, mma_tokens(sub_tokens(tl, 1)), 1, 0);
@@ -252,7 +253,7 @@ __device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb,
             ++l_tile;
         }
         if (l_tile >= tiles) return;
-        const Tile tl = tile_of<kTileTok>(tb, p.w.E, p.num_w, P.pair + l_tile * P.num_pairs);
+        const Tile tl = tile_of(tb, p.w.E, p.num_w, p.cap, P.pair + l_tile * P.num_pairs);
         const int k = tl.row0 + static_cast<int>(P.rank) * kRowsCta + panel * 64 + c * 16;
         l_codes = p.w.codes + static_cast<int64_t>(tl.expert) * N * ld + k;
         l_scale = p.w.scale + static_cast<int64_t>(tl.expert) * N;
@@ -263,21 +264,29 @@ __device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb,
     const int64_t ld8 = static_cast<int64_t>(8) * ld;
     auto issue = [&]() {  // loads the cursor's stage and moves the cursor to this part's next one
         if (l_tile >= tiles) return;
-        const int n0 = l_kb * kBK + (quarter & 1) * 32 + r;
-        const int8_t* src = l_codes + static_cast<int64_t>(n0) * ld;
+        const int n0 = l_kb * kBK + (quarter & 1) * 32;  // the quarter's first row
+        const int8_t* src = l_codes + static_cast<int64_t>(n0 + r) * ld;
+        const float* scale = l_scale + n0 + r;
+        if (l_in && n0 + 32 <= N) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool ok = l_in && n0 + 8 * j < N;  // rows past N are zero (they are part of the contraction)
-            cb[j] = ok ? ldg_codes(src + j * ld8) : make_uint4(0u, 0u, 0u, 0u);
-            sc[j] = ok ? __ldg(l_scale + n0 + 8 * j) : 0.0f;
-        }
-        // this part's next stage but one of the same tile, towards L2: the
-        // loads above are only one of this part's stages ahead
-        if (c == 0 && l_in && l_kb + 2 * kStages < p.kbt) {
-            const int8_t* far = src + static_cast<int64_t>(2 * kStages * kBK) * ld;
+            for (int j = 0; j < 4; ++j) {
+                cb[j] = ldg_codes(src + j * ld8);
+                sc[j] = __ldg(scale + 8 * j);
+            }
+            // this part's next stage but one of the same tile, towards L2: the
+            // loads above are only one of this part's stages ahead
+            if (c == 0 && n0 + 2 * kStages * kBK + 32 <= N) {
+                const int8_t* far = src + static_cast<int64_t>(2 * kStages * kBK) * ld;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (n0 + 2 * kStages * kBK + 8 * j < N) prefetch_l2(far + j * ld8);
+                for (int j = 0; j < 4; ++j) prefetch_l2(far + j * ld8);
+            }
+        } else {  // rows past N are zero (they are part of the contraction)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool ok = l_in && n0 + r + 8 * j < N;
+                cb[j] = ok ? ldg_codes(src + j * ld8) : make_uint4(0u, 0u, 0u, 0u);
+                sc[j] = ok ? __ldg(scale + 8 * j) : 0.0f;
+            }
         }
         l_kb += kStages;
         if (l_kb >= p.kbt) open_tile();
@@ -318,14 +327,14 @@ __device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb,
         // the tiles before this stage's are complete or about to be: write
         // them now, with the next tile's first stages already converted
         while (next_epi < tile) {
-            const Tile tl = tile_of<kTileTok>(tb, p.w.E, p.num_w, P.pair + next_epi * P.num_pairs);
+            const Tile tl = tile_of(tb, p.w.E, p.num_w, p.cap, P.pair + next_epi * P.num_pairs);
             if (!tile_epilogue(P, p, tl, g, part, quarter, lane)) return;
             ++next_epi;
         }
         issue();
     }
     while (next_epi < tiles) {
-        const Tile tl = tile_of<kTileTok>(tb, p.w.E, p.num_w, P.pair + next_epi * P.num_pairs);
+        const Tile tl = tile_of(tb, p.w.E, p.num_w, p.cap, P.pair + next_epi * P.num_pairs);
         if (!tile_epilogue(P, p, tl, g, part, quarter, lane)) return;
         ++next_epi;
     }
@@ -365,7 +374,7 @@ k_int8_dx_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params
     }
     if (warp == 1 && lane == 0)
         for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.y[i]);
-    if (warp == 2) build_table<kTileTok>(p.rr, p.w.E, p.num_w, tb, lane);
+    if (warp == 2) build_table(p.rr, p.w.E, p.num_w, p.cap, tb, lane);
     tc_fence_before();
     __syncthreads();
     cluster_arrive();  // both CTAs' barriers are initialised before any remote arrive
@@ -453,10 +462,26 @@ int max_pairs() {
     return n;
 }
 
+// The most tokens of a tile, by the cycles of 64 n of it (measured: 2.1 a
+// token, 700 at least, the converters' own) times the rounds of tiles, for T
+// rows spread evenly over the experts.  Tiles of 256 occupy twice the pairs
+// where tiles of 512 leave half of them idle (1024 x 4096 x 4096: 41 against
+// 55 us; 4096 x 11008 x 4096: 315 against 246).
+int tile_cap(int64_t T, const Int8Weight& w) {
+    const int64_t experts = T < w.E ? T : w.E, pairs = num_sms() / 2 > 0 ? num_sms() / 2 : 1;
+    const int m = static_cast<int>(ceil_div(T, experts));
+    auto cycles = [&](int cap) {
+        const int64_t tiles = experts * token_tiles(m, cap) * ceil_div(w.K, kTileRows);
+        const int width = token_width(m, cap) * 21 / 10;
+        return ceil_div(tiles, pairs) * (width > 700 ? width : 700);
+    };
+    return cycles(kSubTok) < cycles(kTileTok) ? kSubTok : kTileTok;
+}
+
 }  // namespace
 
 bool int8_dx_supported(int64_t T, const Int8Weight& w) {
-    return int8_tiles(T, w.E, w.K, kTileTok) * ceil_div(w.N, kBK) < (int64_t(1) << 31);
+    return int8_tiles(T, w.E, w.K, kSubTok) * ceil_div(w.N, kBK) < (int64_t(1) << 31);
 }
 
 size_t int8_dx_workspace(int64_t T, const Int8Weight& w) {
@@ -485,12 +510,13 @@ cudaError_t launch_int8_dx(const uint16_t* dY, const Int8Weight& w, const RowRan
     p.rr = rr;
     p.num_w = static_cast<int>(ceil_div(w.K, kTileRows));
     p.kbt = static_cast<int>(ceil_div(w.N, kBK));
+    p.cap = tile_cap(rr.T, w);
     p.dX = dX;
     Maps maps;
     bool ok = true;
     for (int i = 0; i < kBoxes; ++i) ok = ok && make_map_dy(&maps.y[i], dY, w.N, rr.T, ld, box_rows(i));
     if (!ok) return cudaErrorInvalidValue;
-    const int64_t tiles = int8_tiles(rr.T, w.E, w.K, kTileTok);
+    const int64_t tiles = int8_tiles(rr.T, w.E, w.K, p.cap);
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = pair_config(attr, static_cast<int>(tiles < most ? tiles : most), st);
     e = cudaLaunchKernelEx(&cfg, k_int8_dx_pair, maps, p);

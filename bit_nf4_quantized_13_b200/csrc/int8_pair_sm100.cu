@@ -91,7 +91,7 @@ struct Pipe {
 __device__ void role_tma(const Pipe& P, const Params& p, const RowTable& tb, int units, const Maps& maps) {
     int local = 0;
     for (int u = P.pair; u < units; u += P.num_pairs) {
-        const Tile tl = tile_of<kTileTok>(tb, p.E, p.num_w, u);
+        const Tile tl = tile_of(tb, p.E, p.num_w, kTileTok, u);
         const int half = mma_tokens(tl.toks) / 2;
         const int box = box_index(half);
         const int wrow = tl.expert * p.N + tl.row0 + static_cast<int>(P.rank) * kRowsCta;
@@ -122,7 +122,7 @@ __device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, int
     int s = 0, i = 0;
     uint32_t ph = 0;
     for (int u = P.pair; u < units; u += P.num_pairs, ++i) {
-        const Tile tl = tile_of<kTileTok>(tb, p.E, p.num_w, u);
+        const Tile tl = tile_of(tb, p.E, p.num_w, kTileTok, u);
         const int b = i & 1;
         const uint32_t idesc = idesc_i8(kRowsPair, mma_tokens(tl.toks));
         if (!mbar_wait(P.acc_empty(b), (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u, &g_int8_error)) return;
@@ -182,7 +182,7 @@ __device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb
     float* sx = s_sx[warp - 2];
     int i = 0;
     for (int u = P.pair; u < units; u += P.num_pairs, ++i) {
-        const Tile tl = tile_of<kTileTok>(tb, p.E, p.num_w, u);
+        const Tile tl = tile_of(tb, p.E, p.num_w, kTileTok, u);
         const int b = i & 1;
         const int chunks = mma_tokens(tl.toks) / 32;
         const int chan = tl.row0 + static_cast<int>(P.rank) * kRowsCta + quarter * 32 + lane;
@@ -246,7 +246,7 @@ k_int8_gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Para
         tma_prefetch_desc(&maps.w);
         for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.x[i]);
     }
-    if (warp == 2) build_table<kTileTok>(p.rr, p.E, p.num_w, tb, lane);
+    if (warp == 2) build_table(p.rr, p.E, p.num_w, kTileTok, tb, lane);
     tc_fence_before();
     __syncthreads();
     cluster_arrive();  // both CTAs' barriers are initialised before any remote arrive

@@ -21,11 +21,20 @@ __device__ __forceinline__ RowTable row_table(void* smem) {
     return RowTable{static_cast<int*>(smem), static_cast<int*>(smem) + QLORA_MAX_EXPERTS + 1};
 }
 
+// An expert's m token rows are cut into the fewest tiles of at most `cap`
+// tokens, all of the same width (a multiple of 32): 257 rows are two tiles of
+// 160, not one of 256 and one of 32, whose stages cost nearly as much.
+__host__ __device__ inline int token_tiles(int m, int cap) { return (m + cap - 1) / cap; }
+__host__ __device__ inline int token_width(int m, int cap) {
+    const int t = token_tiles(m, cap);
+    return t > 0 ? ((m + t - 1) / t + 31) & ~31 : 0;
+}
+
 // Filled by one warp.  An offset counts as no less than the one before it and
 // at most T, so the ranges are disjoint and inside the rows whatever it holds.
 // num_w: weight-side tiles of one expert.
-template <int kTileTok>
-__device__ __forceinline__ void build_table(const RowRanges& rr, int E, int num_w, const RowTable& tb, int lane) {
+__device__ __forceinline__ void build_table(const RowRanges& rr, int E, int num_w, int cap, const RowTable& tb,
+                                            int lane) {
     const int T = static_cast<int>(rr.T);
     int top = 0, tiles = 0;  // the last offset and the tiles so far
     if (rr.offsets) top = min(max(rr.offsets[0], 0), T);
@@ -42,7 +51,7 @@ __device__ __forceinline__ void build_table(const RowRanges& rr, int E, int num_
         for (int o = 1; o < 32; o <<= 1) hi = max(hi, __shfl_up_sync(0xffffffffu, hi, o));  // lanes < o: their own
         int lo = __shfl_up_sync(0xffffffffu, hi, 1);
         if (lane == 0) lo = top;
-        int n = e < E ? (hi - lo + kTileTok - 1) / kTileTok * num_w : 0;
+        int n = e < E ? token_tiles(hi - lo, cap) * num_w : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int up = __shfl_up_sync(0xffffffffu, n, o);
@@ -65,8 +74,7 @@ struct Tile {
 // Tile `unit`: experts in order; inside an expert bands of kBand weight tiles
 // with the token tiles slowest in a band, so that the pairs at work at the
 // same time cover a compact block of tokens and weights (kept in L2).
-template <int kTileTok>
-__device__ __forceinline__ Tile tile_of(const RowTable& tb, int E, int num_w, int unit) {
+__device__ __forceinline__ Tile tile_of(const RowTable& tb, int E, int num_w, int cap, int unit) {
     constexpr int kBand = 8;
     int e = 0, above = E;  // tile0[e] <= unit < tile0[above]
     while (above - e > 1) {
@@ -78,7 +86,7 @@ __device__ __forceinline__ Tile tile_of(const RowTable& tb, int E, int num_w, in
     }
     const int lo = tb.off[e], hi = tb.off[e + 1];
     const int u = unit - tb.tile0[e];
-    const int num_t = (hi - lo + kTileTok - 1) / kTileTok;
+    const int num_t = token_tiles(hi - lo, cap), width = token_width(hi - lo, cap);
     const int band_tiles = kBand * num_t;
     const int band = u / band_tiles, in = u % band_tiles;
     const int rows_in_band = min(kBand, num_w - band * kBand);
@@ -86,8 +94,8 @@ __device__ __forceinline__ Tile tile_of(const RowTable& tb, int E, int num_w, in
     Tile s;
     s.expert = e;
     s.row0 = (band * kBand + in % rows_in_band) * kTileRows;
-    s.tok0 = lo + t * kTileTok;
-    s.toks = min(kTileTok, hi - s.tok0);
+    s.tok0 = lo + t * width;
+    s.toks = min(width, hi - s.tok0);
     return s;
 }
 
