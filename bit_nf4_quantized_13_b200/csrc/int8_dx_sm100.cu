@@ -71,7 +71,6 @@ struct Params {
     RowRanges rr;
     int num_w;      // column tiles: ceil(K / 256)
     int kbt;        // stages of a tile: ceil(N / 64)
-    int cap;        // most tokens of a tile: kTileTok or kSubTok
     uint16_t* dX;
 };
 
@@ -100,7 +99,7 @@ __device__ __forceinline__ int sub_tokens(const Tile& tl, int sub) {
 __device__ void role_tma(const Pipe& P, const Params& p, const RowTable& tb, int units, const Maps& maps) {
     int local = 0;
     for (int u = P.pair; u < units; u += P.num_pairs) {
-        const Tile tl = tile_of(tb, p.w.E, p.num_w, p.cap, u);
+        const Tile tl = tile_of(tb, p.w.E, p.num_w, kTileTok, u);
         int box[kSubs], row[kSubs];
         uint32_t tx = 0;
         int subs = 0;
@@ -137,7 +136,7 @@ __device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, int
     int s = 0, g = 0;
     uint32_t ph = 0;
     for (int u = P.pair; u < units; u += P.num_pairs) {
-        const Tile tl = tile_of(tb, p.w.E, p.num_w, p.cap, u);
+        const Tile tl = tile_of(tb, p.w.E, p.num_w, kTileTok, u);
         const int subs = tl.toks > kSubTok ? 2 : 1;
         const uint32_t idesc0 = idesc_bf16(kTileRows, mma_tokens(sub_tokens(tl, 0)), 1, 0);
         const uint32_t idesc1 = idesc_bf16(kTileRows, mma_tokens(sub_tokens(tl, 1)), 1, 0);
@@ -176,30 +175,6 @@ __device__ __forceinline__ uint4 ldg_codes(const int8_t* p) {
     return v;
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
-// Four codes -> two bf16 pairs of RN32(code * sc); ms = {sc, sc}.  The fp32
-// steps are done two at a time (each half is the ordinary IEEE operation).
-__device__ __forceinline__ void convert4(uint32_t codes, uint64_t ms, uint32_t& lo, uint32_t& hi) {
-    const uint32_t u = codes ^ 0x80808080u;  // code + 128
-    uint32_t f[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = prmt(u, 0x4B000000u, 0x7540u + i);  // 2^23 + 128 + code
-    asm("{\n\t.reg .b64 a, b, m;\n\t"
-        "mov.b64 a, {%2, %3};\n\t"
-        "mov.b64 b, {%4, %5};\n\t"
-        "mov.b64 m, {%7, %7};\n\t"
-        "add.rn.f32x2 a, a, m;\n\t"
-        "add.rn.f32x2 b, b, m;\n\t"
-        "mul.rn.f32x2 a, a, %6;\n\t"
-        "mul.rn.f32x2 b, b, %6;\n\t"
-        ".reg .f32 a0, a1, b0, b1;\n\t"
-        "mov.b64 {a0, a1}, a;\n\t"
-        "mov.b64 {b0, b1}, b;\n\t"
-        "cvt.rn.bf16x2.f32 %0, a1, a0;\n\t"
-        "cvt.rn.bf16x2.f32 %1, b1, b0;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3]), "l"(ms), "r"(0xCB000080u /* -(2^23 + 128) */));
-}
 
 // Outputs of the tile `tl`, whose accumulators are the g-th and following:
 // this warp's TMEM lane quarter, every fourth 32-token chunk.
@@ -253,7 +228,7 @@ __device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb,
             ++l_tile;
         }
         if (l_tile >= tiles) return;
-        const Tile tl = tile_of(tb, p.w.E, p.num_w, p.cap, P.pair + l_tile * P.num_pairs);
+        const Tile tl = tile_of(tb, p.w.E, p.num_w, kTileTok, P.pair + l_tile * P.num_pairs);
         const int k = tl.row0 + static_cast<int>(P.rank) * kRowsCta + panel * 64 + c * 16;
         l_codes = p.w.codes + static_cast<int64_t>(tl.expert) * N * ld + k;
         l_scale = p.w.scale + static_cast<int64_t>(tl.expert) * N;
@@ -327,14 +302,14 @@ __device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb,
         // the tiles before this stage's are complete or about to be: write
         // them now, with the next tile's first stages already converted
         while (next_epi < tile) {
-            const Tile tl = tile_of(tb, p.w.E, p.num_w, p.cap, P.pair + next_epi * P.num_pairs);
+            const Tile tl = tile_of(tb, p.w.E, p.num_w, kTileTok, P.pair + next_epi * P.num_pairs);
             if (!tile_epilogue(P, p, tl, g, part, quarter, lane)) return;
             ++next_epi;
         }
         issue();
     }
     while (next_epi < tiles) {
-        const Tile tl = tile_of(tb, p.w.E, p.num_w, p.cap, P.pair + next_epi * P.num_pairs);
+        const Tile tl = tile_of(tb, p.w.E, p.num_w, kTileTok, P.pair + next_epi * P.num_pairs);
         if (!tile_epilogue(P, p, tl, g, part, quarter, lane)) return;
         ++next_epi;
     }
@@ -374,7 +349,7 @@ k_int8_dx_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params
     }
     if (warp == 1 && lane == 0)
         for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.y[i]);
-    if (warp == 2) build_table(p.rr, p.w.E, p.num_w, p.cap, tb, lane);
+    if (warp == 2) build_table(p.rr, p.w.E, p.num_w, kTileTok, tb, lane);
     tc_fence_before();
     __syncthreads();
     cluster_arrive();  // both CTAs' barriers are initialised before any remote arrive
@@ -462,20 +437,24 @@ int max_pairs() {
     return n;
 }
 
-// The most tokens of a tile, by the cycles of 64 n of it (measured: 2.1 a
-// token, 700 at least, the converters' own) times the rounds of tiles, for T
-// rows spread evenly over the experts.  Tiles of 256 occupy twice the pairs
-// where tiles of 512 leave half of them idle (1024 x 4096 x 4096: 41 against
-// 55 us; 4096 x 11008 x 4096: 315 against 246).
+// The most tokens of a tile: kTileTok (this kernel) or kSubTok (the narrow
+// one).  Dense: the fewer cycles, by the measured cost of 64 n of a tile (this
+// kernel 2.1 a token, 800 at least; the narrow one 2.8, 475 at least) times
+// the rounds of tiles.  512 x 5120 x 5120 takes 61 us here and 41 there, 4096 x
+// 11008 x 4096 246 and 266.  Experts: ragged rows fill wide tiles badly and
+// level out better in small ones (eight experts of 11008 x 4096 with 57 to 1540
+// of 4096 rows: 334 and 309 us), so wide tiles are left to experts of 1024 rows
+// and more on average.
 int tile_cap(int64_t T, const Int8Weight& w) {
-    const int64_t experts = T < w.E ? T : w.E, pairs = num_sms() / 2 > 0 ? num_sms() / 2 : 1;
-    const int m = static_cast<int>(ceil_div(T, experts));
-    auto cycles = [&](int cap) {
-        const int64_t tiles = experts * token_tiles(m, cap) * ceil_div(w.K, kTileRows);
-        const int width = token_width(m, cap) * 21 / 10;
-        return ceil_div(tiles, pairs) * (width > 700 ? width : 700);
+    if (w.E > 1) return T < 1024 * static_cast<int64_t>(w.E) ? kSubTok : kTileTok;
+    const int64_t pairs = num_sms() / 2 > 0 ? num_sms() / 2 : 1;
+    const int m = static_cast<int>(T);
+    auto rounds = [&](int cap) { return ceil_div(token_tiles(m, cap) * ceil_div(w.K, kTileRows), pairs); };
+    auto cost = [&](int cap, int tenths, int least) {
+        const int c = token_width(m, cap) * tenths / 10;
+        return c > least ? c : least;
     };
-    return cycles(kSubTok) < cycles(kTileTok) ? kSubTok : kTileTok;
+    return rounds(kSubTok) * cost(kSubTok, 28, 475) <= rounds(kTileTok) * cost(kTileTok, 21, 800) ? kSubTok : kTileTok;
 }
 
 }  // namespace
@@ -490,11 +469,7 @@ size_t int8_dx_workspace(int64_t T, const Int8Weight& w) {
 
 cudaError_t launch_int8_dx(const uint16_t* dY, const Int8Weight& w, const RowRanges& rr, uint16_t* dX, void* ws,
                            cudaStream_t st) {
-    static ContextMemo<int> attr_memo;
-    cudaError_t e = ensure_smem_limit(attr_memo, k_int8_dx_pair, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    const int most = max_pairs();
-    if (most <= 0) return cudaErrorNotSupported;
+    cudaError_t e;
     const int64_t ld = round_up(w.N, 8);
     if (ld != w.N) {
         const int64_t cap = static_cast<int64_t>(num_sms()) * 8;
@@ -505,18 +480,23 @@ cudaError_t launch_int8_dx(const uint16_t* dY, const Int8Weight& w, const RowRan
         if (e != cudaSuccess) return e;
         dY = static_cast<const uint16_t*>(ws);
     }
+    if (tile_cap(rr.T, w) == kSubTok) return launch_int8_dx_narrow(dY, ld, w, rr, dX, st);
+    static ContextMemo<int> attr_memo;
+    e = ensure_smem_limit(attr_memo, k_int8_dx_pair, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    const int most = max_pairs();
+    if (most <= 0) return cudaErrorNotSupported;
     Params p{};
     p.w = w;
     p.rr = rr;
     p.num_w = static_cast<int>(ceil_div(w.K, kTileRows));
     p.kbt = static_cast<int>(ceil_div(w.N, kBK));
-    p.cap = tile_cap(rr.T, w);
     p.dX = dX;
     Maps maps;
     bool ok = true;
     for (int i = 0; i < kBoxes; ++i) ok = ok && make_map_dy(&maps.y[i], dY, w.N, rr.T, ld, box_rows(i));
     if (!ok) return cudaErrorInvalidValue;
-    const int64_t tiles = int8_tiles(rr.T, w.E, w.K, p.cap);
+    const int64_t tiles = int8_tiles(rr.T, w.E, w.K, kTileTok);
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = pair_config(attr, static_cast<int>(tiles < most ? tiles : most), st);
     e = cudaLaunchKernelEx(&cfg, k_int8_dx_pair, maps, p);

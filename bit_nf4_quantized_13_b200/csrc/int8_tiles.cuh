@@ -112,6 +112,30 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     return r;
 }
 
+// Four codes -> two bf16 pairs of RN32(code * sc); ms = {sc, sc}.  The fp32
+// steps are done two at a time (each half is the ordinary IEEE operation).
+__device__ __forceinline__ void convert4(uint32_t codes, uint64_t ms, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = codes ^ 0x80808080u;  // code + 128
+    uint32_t f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = prmt(u, 0x4B000000u, 0x7540u + i);  // 2^23 + 128 + code
+    asm("{\n\t.reg .b64 a, b, m;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "mov.b64 m, {%7, %7};\n\t"
+        "add.rn.f32x2 a, a, m;\n\t"
+        "add.rn.f32x2 b, b, m;\n\t"
+        "mul.rn.f32x2 a, a, %6;\n\t"
+        "mul.rn.f32x2 b, b, %6;\n\t"
+        ".reg .f32 a0, a1, b0, b1;\n\t"
+        "mov.b64 {a0, a1}, a;\n\t"
+        "mov.b64 {b0, b1}, b;\n\t"
+        "cvt.rn.bf16x2.f32 %0, a1, a0;\n\t"
+        "cvt.rn.bf16x2.f32 %1, b1, b0;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3]), "l"(ms), "r"(0xCB000080u /* -(2^23 + 128) */));
+}
+
 // Stores 32 tokens x 32 columns of a row-major bf16 matrix: lane `lane` holds
 // column `col` (= col0 + lane, col0 a multiple of 32) of the tokens 0 .. 31 as
 // v[]; `left` of the tokens exist.  Rows whose length is a multiple of 4 are
