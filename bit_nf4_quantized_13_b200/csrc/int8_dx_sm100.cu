@@ -454,7 +454,8 @@ int tile_cap(int64_t T, const Int8Weight& w) {
         const int c = token_width(m, cap) * tenths / 10;
         return c > least ? c : least;
     };
-    return rounds(kSubTok) * cost(kSubTok, 28, 475) <= rounds(kTileTok) * cost(kTileTok, 21, 800) ? kSubTok : kTileTok;
+    const int64_t narrow = rounds(kSubTok) * cost(kSubTok, 28, 475) / int8_dx_narrow_parts(T, w);
+    return narrow <= rounds(kTileTok) * cost(kTileTok, 21, 800) ? kSubTok : kTileTok;
 }
 
 }  // namespace
@@ -463,8 +464,14 @@ bool int8_dx_supported(int64_t T, const Int8Weight& w) {
     return int8_tiles(T, w.E, w.K, kSubTok) * ceil_div(w.N, kBK) < (int64_t(1) << 31);
 }
 
+// Workspace: dY's rows padded to 16 bytes, where N is not a multiple of 8, then
+// the narrow kernel's.
+size_t dx_padded_bytes(int64_t T, const Int8Weight& w) {
+    return w.N % 8 == 0 ? 0 : static_cast<size_t>(round_up(T * round_up(w.N, 8) * 2, 256));
+}
+
 size_t int8_dx_workspace(int64_t T, const Int8Weight& w) {
-    return w.N % 8 == 0 ? 0 : static_cast<size_t>(T) * static_cast<size_t>(round_up(w.N, 8)) * 2;
+    return dx_padded_bytes(T, w) + (tile_cap(T, w) == kSubTok ? int8_dx_narrow_workspace(T, w) : 0);
 }
 
 cudaError_t launch_int8_dx(const uint16_t* dY, const Int8Weight& w, const RowRanges& rr, uint16_t* dX, void* ws,
@@ -480,7 +487,8 @@ cudaError_t launch_int8_dx(const uint16_t* dY, const Int8Weight& w, const RowRan
         if (e != cudaSuccess) return e;
         dY = static_cast<const uint16_t*>(ws);
     }
-    if (tile_cap(rr.T, w) == kSubTok) return launch_int8_dx_narrow(dY, ld, w, rr, dX, st);
+    if (tile_cap(rr.T, w) == kSubTok)
+        return launch_int8_dx_narrow(dY, ld, w, rr, dX, static_cast<char*>(ws) + dx_padded_bytes(rr.T, w), st);
     static ContextMemo<int> attr_memo;
     e = ensure_smem_limit(attr_memo, k_int8_dx_pair, kSmemBytes);
     if (e != cudaSuccess) return e;

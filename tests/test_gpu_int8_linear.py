@@ -120,7 +120,8 @@ def test_linear_fwd(M, N, K, dtype):
                                    (64, 8, 640), (100, 3, 128), (130, 4097, 192), (255, 129, 257), (300, 1024, 520),
                                    (512, 640, 384), (513, 72, 2049), (700, 333, 777), (1025, 1280, 2048),
                                    (2049, 2304, 1024), (256, 192, 9500), (257, 8, 96), (4608, 200, 4096),
-                                   (4700, 68, 4100), (2600, 1, 8000)])
+                                   (4700, 68, 4100), (2600, 1, 8000), (1, 4096, 64), (40, 5000, 300), (300, 4100, 200),
+                                   (257, 11008, 48)])
 def test_linear_bwd(M, N, K):
     dY, w = tokens(M * 3 + N, M, N, 0.01), weight(K + 1, N, K)
     dX = q.qlora_int8_linear_bwd(dY, w)
@@ -220,6 +221,8 @@ EXPERT_CASES = [
     ([0, 1] * 500, 5, 5, 17, 33),
     ([3900, 100, 0, 150], 1, 3, 72, 300),   # 1024 rows an expert and more: wide gradient tiles, and small ones among them
     ([1500, 2600, 1025], 0, 0, 65, 513),
+    ([5, 0, 30], 2, 1, 5000, 130),          # few tiles, a long contraction of the gradient
+    ([300, 20], 0, 4, 4097, 64),
 ]
 
 
