@@ -81,15 +81,17 @@ def _load() -> ctypes.CDLL:
         "qlora_int8_quantize": (i32, [vp, i64, i32, vp, vp, vp, vp]),
         "qlora_int8_dequantize": (i32, [vp, vp, i64, i32, vp, vp]),
         "qlora_int8_quantize_rows": (i32, [vp, i32, i64, i64, vp, vp, vp, vp]),
+        "qlora_int8_matmul_workspace_size": (sz, [i64, i64, i64]),
+        "qlora_int8_expert_matmul_workspace_size": (sz, [i64, i32, i64, i64]),
         "qlora_int8_linear_fwd_workspace_size": (sz, [i64, i64, i64]),
         "qlora_int8_linear_bwd_workspace_size": (sz, [i64, i64, i64]),
         "qlora_int8_linear_fwd": (i32, [vp, i64, i64, i64, vp, vp, vp, i32, vp, sz, vp]),
-        "qlora_int8_matmul": (i32, [vp, vp, i64, i64, i64, vp, vp, vp, i32, vp]),
+        "qlora_int8_matmul": (i32, [vp, vp, i64, i64, i64, vp, vp, vp, i32, vp, sz, vp]),
         "qlora_int8_linear_bwd": (i32, [vp, i64, i64, i64, vp, vp, vp, vp, sz, vp]),
         "qlora_int8_expert_fwd_workspace_size": (sz, [i64, i32, i64, i64]),
         "qlora_int8_expert_bwd_workspace_size": (sz, [i64, i32, i64, i64]),
         "qlora_int8_expert_fwd": (i32, [vp, vp, i64, i32, i64, i64, vp, vp, vp, i32, vp, sz, vp]),
-        "qlora_int8_expert_matmul": (i32, [vp, vp, vp, i64, i32, i64, i64, vp, vp, vp, i32, vp]),
+        "qlora_int8_expert_matmul": (i32, [vp, vp, vp, i64, i32, i64, i64, vp, vp, vp, i32, vp, sz, vp]),
         "qlora_int8_expert_bwd": (i32, [vp, vp, i64, i32, i64, i64, vp, vp, vp, vp, sz, vp]),
         "qlora_debug_fill": (i32, [vp, i64, ctypes.c_uint32, vp]),
         "qlora_debug_read": (i32, [vp, i64, ctypes.c_uint32, vp, vp]),
@@ -617,6 +619,16 @@ def qlora_int8_linear_bwd_workspace_size(M, N, K) -> int:
     return int(_get_lib().qlora_int8_linear_bwd_workspace_size(int(M), int(N), int(K)))
 
 
+def qlora_int8_matmul_workspace_size(M, N, K) -> int:
+    """Workspace of qlora_int8_linear_fwd for tokens quantized before."""
+    return int(_get_lib().qlora_int8_matmul_workspace_size(int(M), int(N), int(K)))
+
+
+def qlora_int8_expert_matmul_workspace_size(T, E, N, K) -> int:
+    """Workspace of qlora_int8_expert_fwd for tokens quantized before."""
+    return int(_get_lib().qlora_int8_expert_matmul_workspace_size(int(T), int(E), int(N), int(K)))
+
+
 def qlora_int8_expert_fwd_workspace_size(T, E, N, K) -> int:
     return int(_get_lib().qlora_int8_expert_fwd_workspace_size(int(T), int(E), int(N), int(K)))
 
@@ -675,28 +687,19 @@ def _int8_fwd(X, w, offsets, out_dtype, Y, ws, stream):
     code = 0 if out_dtype == torch.float32 else 1
     quantized = isinstance(X, Int8Rows)
     wc, wsc = w.codes, w.scale
-    # addresses go as plain integers: a ctypes object for each costs more than the check of a call
-    if quantized:
-        _need_cuda(X.codes, X.scale, wc, wsc, offsets, Y)
-        Y, _ = _int8_buffers(Y, (T, N), out_dtype, None, 0, wsc, stream)
-        tail = (wc.data_ptr(), wsc.data_ptr(), Y.data_ptr(), code, _stream(stream))
-        if offsets is None:
-            fn, st = "qlora_int8_matmul", lib.qlora_int8_matmul(X.codes.data_ptr(), X.scale.data_ptr(), T, N, K, *tail)
-        else:
-            fn, st = "qlora_int8_expert_matmul", lib.qlora_int8_expert_matmul(
-                X.codes.data_ptr(), X.scale.data_ptr(), offsets.data_ptr(), T, E, N, K, *tail)
+    x = (X.codes, X.scale) if quantized else (X,)
+    _need_cuda(*x, wc, wsc, offsets, Y, ws)
+    if offsets is None:
+        fn = "qlora_int8_matmul" if quantized else "qlora_int8_linear_fwd"
+        sizes = (T, N, K)
     else:
-        _need_cuda(X, wc, wsc, offsets, Y, ws)
-        need = (lib.qlora_int8_linear_fwd_workspace_size(T, N, K) if offsets is None
-                else lib.qlora_int8_expert_fwd_workspace_size(T, E, N, K))
-        Y, ws = _int8_buffers(Y, (T, N), out_dtype, ws, need, wsc, stream)
-        tail = (wc.data_ptr(), wsc.data_ptr(), Y.data_ptr(), code, None if ws is None else ws.data_ptr(),
-                0 if ws is None else ws.numel(), _stream(stream))
-        if offsets is None:
-            fn, st = "qlora_int8_linear_fwd", lib.qlora_int8_linear_fwd(X.data_ptr(), T, N, K, *tail)
-        else:
-            fn, st = "qlora_int8_expert_fwd", lib.qlora_int8_expert_fwd(X.data_ptr(), offsets.data_ptr(), T, E, N, K,
-                                                                        *tail)
+        fn = "qlora_int8_expert_matmul" if quantized else "qlora_int8_expert_fwd"
+        sizes = (T, E, N, K)
+    Y, ws = _int8_buffers(Y, (T, N), out_dtype, ws, getattr(lib, fn + "_workspace_size")(*sizes), wsc, stream)
+    # addresses go as plain integers: a ctypes object for each costs more than the checks of a call
+    st = getattr(lib, fn)(*[t.data_ptr() for t in x], *(() if offsets is None else (offsets.data_ptr(),)), *sizes,
+                          wc.data_ptr(), wsc.data_ptr(), Y.data_ptr(), code, None if ws is None else ws.data_ptr(),
+                          0 if ws is None else ws.numel(), _stream(stream))
     if st != QLORA_OK:
         _check(fn, st)
     return Y

@@ -395,16 +395,18 @@ int check_int8(int64_t T, int E, int64_t N, int64_t K, bool by_expert, const int
 }
 
 // Workspace of the forward: the tokens' codes and their scales (nothing where
-// the kernel quantizes them itself).
+// they are given, or quantized in the product's kernel), then the product's.
 size_t int8_codes_bytes(int64_t T, int64_t K) { return align256(static_cast<size_t>(T) * int8_row_bytes(K)); }
-size_t int8_fwd_ws(int64_t T, int E, int64_t N, int64_t K) {
-    if (check_int8(T, E, N, K, false, nullptr) != QLORA_OK) return 0;
+size_t int8_fwd_ws(int64_t T, int E, int64_t N, int64_t K, bool quantized) {
+    if (check_int8(T, E, N, K, false, nullptr) != QLORA_OK || T == 0) return 0;
     const Int8Weight w{nullptr, nullptr, E, N, K, int8_row_bytes(K)};
-    if (T == 0 || int8_gemv_fused(T, w)) return 0;
-    return int8_codes_bytes(T, K) + align256(static_cast<size_t>(T) * 4);
+    const size_t rows = quantized || int8_gemv_fused(T, w)
+                            ? 0
+                            : int8_codes_bytes(T, K) + align256(static_cast<size_t>(T) * 4);
+    return rows + (int8_gemv_pays(T, w) ? 0 : int8_pair_workspace(T, w));
 }
 size_t int8_bwd_ws(int64_t T, int E, int64_t N, int64_t K) {
-    if (check_int8(T, E, N, K, false, nullptr) != QLORA_OK) return 0;
+    if (check_int8(T, E, N, K, false, nullptr) != QLORA_OK || T == 0) return 0;
     return int8_dx_workspace(T, Int8Weight{nullptr, nullptr, E, N, K, int8_row_bytes(K)});
 }
 
@@ -419,7 +421,7 @@ int int8_fwd(const uint16_t* X, const int8_t* x_codes, const float* x_scale, con
     if (!ok_ptr(w_codes) || !ok_ptr(w_scale)) return QLORA_ERR_INVALID_ARG;
     if (T == 0) return QLORA_OK;
     if (!ok_ptr(Y) || (quantized ? !ok_ptr(x_codes) || !ok_ptr(x_scale) : !ok_ptr(X))) return QLORA_ERR_INVALID_ARG;
-    const size_t need = quantized ? 0 : int8_fwd_ws(T, E, N, K);
+    const size_t need = int8_fwd_ws(T, E, N, K, quantized);
     if (need > 0 && (!ws || !aligned16(ws) || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
     const Int8Weight w{w_codes, w_scale, E, N, K, int8_row_bytes(K)};
     const RowRanges rr{offsets, T};
@@ -428,16 +430,18 @@ int int8_fwd(const uint16_t* X, const int8_t* x_codes, const float* x_scale, con
     cudaStream_t cs = as_stream(stream);
     if (!quantized && int8_gemv_fused(T, w))
         return cuda_status(launch_int8_fwd_gemv(X, nullptr, nullptr, w, rr, Y, out_dtype, cs, false));
+    char* gws = static_cast<char*>(ws);  // the product's workspace
     if (!quantized) {
         int8_t* xc = static_cast<int8_t*>(ws);
         float* xs = reinterpret_cast<float*>(xc + int8_codes_bytes(T, K));
+        gws = reinterpret_cast<char*>(xs) + align256(static_cast<size_t>(T) * 4);
         const cudaError_t e = launch_int8_rows(X, 1, T, K, xc, xs, nullptr, cs);
         if (e != cudaSuccess) return cuda_status(e);
         x_codes = xc;
         x_scale = xs;
     }
     if (few) return cuda_status(launch_int8_fwd_gemv(nullptr, x_codes, x_scale, w, rr, Y, out_dtype, cs, !quantized));
-    return pair_status(launch_int8_fwd_pair(x_codes, x_scale, w, rr, Y, out_dtype, cs, !quantized));
+    return pair_status(launch_int8_fwd_pair(x_codes, x_scale, w, rr, Y, out_dtype, gws, cs, !quantized));
 }
 
 int int8_bwd(const uint16_t* dY, const int32_t* offsets, bool by_expert, int64_t T, int E, int64_t N, int64_t K,
@@ -468,9 +472,15 @@ int qlora_int8_quantize_rows(const void* x, int x_dtype, int64_t rows, int64_t K
     return cuda_status(launch_int8_rows(x, x_dtype, rows, K, codes, scale, status, as_stream(stream)));
 }
 
-size_t qlora_int8_linear_fwd_workspace_size(int64_t M, int64_t N, int64_t K) { return int8_fwd_ws(M, 1, N, K); }
+size_t qlora_int8_matmul_workspace_size(int64_t M, int64_t N, int64_t K) { return int8_fwd_ws(M, 1, N, K, true); }
+size_t qlora_int8_linear_fwd_workspace_size(int64_t M, int64_t N, int64_t K) { return int8_fwd_ws(M, 1, N, K, false); }
 size_t qlora_int8_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K) { return int8_bwd_ws(M, 1, N, K); }
-size_t qlora_int8_expert_fwd_workspace_size(int64_t T, int E, int64_t N, int64_t K) { return int8_fwd_ws(T, E, N, K); }
+size_t qlora_int8_expert_matmul_workspace_size(int64_t T, int E, int64_t N, int64_t K) {
+    return int8_fwd_ws(T, E, N, K, true);
+}
+size_t qlora_int8_expert_fwd_workspace_size(int64_t T, int E, int64_t N, int64_t K) {
+    return int8_fwd_ws(T, E, N, K, false);
+}
 size_t qlora_int8_expert_bwd_workspace_size(int64_t T, int E, int64_t N, int64_t K) { return int8_bwd_ws(T, E, N, K); }
 
 int qlora_int8_linear_fwd(const uint16_t* X, int64_t M, int64_t N, int64_t K, const int8_t* w_codes,
@@ -480,9 +490,10 @@ int qlora_int8_linear_fwd(const uint16_t* X, int64_t M, int64_t N, int64_t K, co
 }
 
 int qlora_int8_matmul(const int8_t* x_codes, const float* x_scale, int64_t M, int64_t N, int64_t K,
-                      const int8_t* w_codes, const float* w_scale, void* Y, int out_dtype, void* stream) {
-    return int8_fwd(nullptr, x_codes, x_scale, nullptr, false, true, M, 1, N, K, w_codes, w_scale, Y, out_dtype,
-                    nullptr, 0, stream);
+                      const int8_t* w_codes, const float* w_scale, void* Y, int out_dtype, void* ws,
+                      size_t ws_bytes, void* stream) {
+    return int8_fwd(nullptr, x_codes, x_scale, nullptr, false, true, M, 1, N, K, w_codes, w_scale, Y, out_dtype, ws,
+                    ws_bytes, stream);
 }
 
 int qlora_int8_linear_bwd(const uint16_t* dY, int64_t M, int64_t N, int64_t K, const int8_t* w_codes,
@@ -499,9 +510,9 @@ int qlora_int8_expert_fwd(const uint16_t* X, const int32_t* offsets, int64_t T, 
 
 int qlora_int8_expert_matmul(const int8_t* x_codes, const float* x_scale, const int32_t* offsets, int64_t T, int E,
                              int64_t N, int64_t K, const int8_t* w_codes, const float* w_scale, void* Y,
-                             int out_dtype, void* stream) {
-    return int8_fwd(nullptr, x_codes, x_scale, offsets, true, true, T, E, N, K, w_codes, w_scale, Y, out_dtype,
-                    nullptr, 0, stream);
+                             int out_dtype, void* ws, size_t ws_bytes, void* stream) {
+    return int8_fwd(nullptr, x_codes, x_scale, offsets, true, true, T, E, N, K, w_codes, w_scale, Y, out_dtype, ws,
+                    ws_bytes, stream);
 }
 
 int qlora_int8_expert_bwd(const uint16_t* dY, const int32_t* offsets, int64_t T, int E, int64_t N, int64_t K,

@@ -23,12 +23,6 @@
 // (the load of 4 neighbouring pieces) and in bit 0 (the store of every second
 // piece): neither has bank conflicts.
 //
-// Where the tiles leave most pairs idle (few columns, a long contraction) each
-// tile's stages are cut into `parts` runs for as many pairs.  Every part leaves
-// its fp32 sums in a workspace slot of its own and a second kernel adds them in
-// order, so no pair waits for another and the result does not depend on the
-// order of arrival.
-//
 // Every mbarrier wait is bounded; a timeout records QLORA_ERR_TIMEOUT in a
 // sticky device word and ends the role.
 #include <cudaTypedefs.h>
@@ -71,37 +65,10 @@ constexpr uint16_t kPairMask = 0x3;
 
 struct Params {
     const float* scale;  // E x N
-    RowRanges rr;
-    int E, N, K;
-    int num_w;           // column tiles: ceil(K / 256)
-    int kbt;             // stages of a tile: ceil(N / 64)
-    int parts;           // parts of a tile
+    Schedule q;          // column tiles: ceil(K / 256); stages: ceil(N / 64)
+    int N, K;
     uint16_t* dX;
-    float* slots;        // parts > 1: the parts' sums
-    int64_t slot_words;
 };
-
-// One part of a tile.
-struct Item {
-    Tile tl;
-    int kb0, stages;
-};
-
-__device__ __forceinline__ Item item_of(const Params& p, const RowTable& tb, int it) {
-    Item x;
-    x.tl = tile_of(tb, p.E, p.num_w, kTileTok, it / p.parts);
-    const int part = it % p.parts;
-    x.kb0 = part * p.kbt / p.parts;
-    x.stages = (part + 1) * p.kbt / p.parts - x.kb0;
-    return x;
-}
-
-// A slot holds [CTA][chunk of 32 tokens][group of 4 tokens][row][4], so that
-// each lane's 16 bytes of a group are part of 512 contiguous ones.
-__device__ __forceinline__ float4* slot_at(const Params& p, int slot, uint32_t rank, int chunk, int group, int row) {
-    return reinterpret_cast<float4*>(p.slots + slot * p.slot_words + rank * (p.slot_words / 2) +
-                                     (static_cast<int64_t>(chunk * 8 + group) * kRowsCta + row) * 4);
-}
 
 struct Maps {
     CUtensorMap w;          // codes: boxes of 64 n x 128 k
@@ -142,7 +109,7 @@ struct Ring {
 __device__ void role_tokens(const Pipe& P, const Params& p, const RowTable& tb, int items, const Maps& maps) {
     Ring<kStages> ring{0, 1};
     for (int it = P.pair; it < items; it += P.num_pairs) {
-        const Item x = item_of(p, tb, it);
+        const Item x = item_of(p.q, tb, kTileTok, it);
         const Tile& tl = x.tl;
         const int half = mma_tokens(tl.toks) / 2, box = box_index(half);
         const int row = tl.tok0 + static_cast<int>(P.rank) * half;
@@ -158,7 +125,7 @@ __device__ void role_tokens(const Pipe& P, const Params& p, const RowTable& tb, 
 __device__ void role_codes(const Pipe& P, const Params& p, const RowTable& tb, int items, const Maps& maps) {
     Ring<kRaw> ring{0, 1};
     for (int it = P.pair; it < items; it += P.num_pairs) {
-        const Item x = item_of(p, tb, it);
+        const Item x = item_of(p.q, tb, kTileTok, it);
         const int col = x.tl.row0 + static_cast<int>(P.rank) * kRowsCta, n0 = x.tl.expert * p.N;
         for (int kb = x.kb0; kb < x.kb0 + x.stages; ++kb, ring.step(1)) {
             if (!mbar_wait(P.raw_empty(ring.slot), ring.turn, &g_int8_dx_narrow_error)) return;
@@ -179,7 +146,7 @@ __device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, int
     Ring<kStages> ring{0, 0};
     int i = 0;
     for (int it = P.pair; it < items; it += P.num_pairs, ++i) {
-        const Item x = item_of(p, tb, it);
+        const Item x = item_of(p.q, tb, kTileTok, it);
         const uint32_t idesc = idesc_bf16(kTileRows, mma_tokens(x.tl.toks), 1, 0);
         const int b = i & 1;
         if (!mbar_wait(P.acc_empty(b), (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u, &g_int8_dx_narrow_error)) return;
@@ -223,7 +190,7 @@ __device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb,
     uint32_t turn = 1;
     int kb = part;  // this part's next stage, counted from the item's first
     for (int it = P.pair; it < items; it += P.num_pairs) {
-        const Item x = item_of(p, tb, it);
+        const Item x = item_of(p.q, tb, kTileTok, it);
         const float* scale = p.scale + static_cast<int64_t>(x.tl.expert) * p.N;
         for (; kb < x.stages; kb += kParts) {
             // rows past N hold other codes or zeros: scale 0 makes them 0
@@ -266,8 +233,11 @@ __device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb,
 }
 
 // This thread's 32 sums (tokens tok .. of column `col`) to dX.
-__device__ __forceinline__ void store_sums(const Params& p, const float (&v)[32], const Tile& tl, int tok, int col,
-                                           int lane) {
+__device__ __forceinline__ void store_sums(const Params& p, const uint32_t (&sums)[32], const Tile& tl, int tok,
+                                           int col, int lane) {
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(sums[j]);
     store_bf16_chunk(p.dX + static_cast<int64_t>(tl.tok0 + tok) * p.K, p.K, col, tl.toks - tok, v, lane);
 }
 
@@ -275,7 +245,7 @@ __device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     int i = 0;
     for (int it = P.pair; it < items; it += P.num_pairs, ++i) {
-        const Item x = item_of(p, tb, it);
+        const Item x = item_of(p.q, tb, kTileTok, it);
         const int b = i & 1, row = quarter * 32 + lane;
         if (!warp_wait(P.acc_full(b), static_cast<uint32_t>(i >> 1) & 1u)) return;
         tc_fence_after();
@@ -284,17 +254,10 @@ __device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb
             uint32_t acc[32];
             tmem_ld_32x32b_x32(P.tmem + lane_base + static_cast<uint32_t>(b * kTileTok + tok), acc);
             tmem_wait_ld();
-            float v[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(acc[j]);
-            if (p.parts == 1) {
-                store_sums(p, v, x.tl, tok, x.tl.row0 + static_cast<int>(P.rank) * kRowsCta + row, lane);
-            } else {
-#pragma unroll
-                for (int g = 0; g < 8; ++g)
-                    *slot_at(p, it, P.rank, tok / 32, g, row) =
-                        make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
-            }
+            if (p.q.parts == 1)
+                store_sums(p, acc, x.tl, tok, x.tl.row0 + static_cast<int>(P.rank) * kRowsCta + row, lane);
+            else
+                slot_store(p.q, it, P.rank, tok / 32, row, acc);
         }
         tc_fence_before();
         __syncwarp();
@@ -342,14 +305,14 @@ k_int8_dx_narrow(const __grid_constant__ Maps maps, const __grid_constant__ Para
         tma_prefetch_desc(&maps.w);
         for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.y[i]);
     }
-    if (warp == 2) build_table(p.rr, p.E, p.num_w, kTileTok, tb, lane);
+    if (warp == 2) build_table(p.q.rr, p.q.E, p.q.num_w, kTileTok, tb, lane);
     tc_fence_before();
     __syncthreads();
     cluster_arrive();  // both CTAs' barriers are initialised before any remote arrive
     cluster_wait();
     tc_fence_after();
     P.tmem = *tmem_slot;
-    const int items = tb.tile0[p.E] * p.parts;
+    const int items = tb.tile0[p.q.E] * p.q.parts;
     if (warp == 0) {
         if (elect_one()) role_tokens(P, p, tb, items, maps);
     } else if (warp == 1) {
@@ -379,34 +342,12 @@ k_int8_dx_narrow(const __grid_constant__ Maps maps, const __grid_constant__ Para
     }
 }
 
-// Adds the parts of tile blockIdx.x, chunk blockIdx.y of 32 tokens, for the
-// rows of CTA blockIdx.z: a thread a row.
-__global__ void __launch_bounds__(kRowsCta) k_int8_dx_parts(const __grid_constant__ Params p) {
-    __shared__ int s_table[kRowTableBytes / 4];
-    const RowTable tb = row_table(s_table);
-    if (threadIdx.x < 32) build_table(p.rr, p.E, p.num_w, kTileTok, tb, static_cast<int>(threadIdx.x));
-    __syncthreads();
-    const int tile = static_cast<int>(blockIdx.x), chunk = static_cast<int>(blockIdx.y);
-    const int row = static_cast<int>(threadIdx.x);
-    grid_dependency_wait();  // the parts' sums
-    if (tile >= tb.tile0[p.E]) return;
-    const Tile tl = tile_of(tb, p.E, p.num_w, kTileTok, tile);
-    if (chunk * 32 >= tl.toks) return;
-    float v[32] = {};
-#pragma unroll 2
-    for (int j = 0; j < p.parts; ++j) {
-        float4 x[8];
-#pragma unroll
-        for (int g = 0; g < 8; ++g) x[g] = __ldcg(slot_at(p, tile * p.parts + j, blockIdx.z, chunk, g, row));
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-            v[4 * g] += x[g].x;
-            v[4 * g + 1] += x[g].y;
-            v[4 * g + 2] += x[g].z;
-            v[4 * g + 3] += x[g].w;
-        }
-    }
-    store_sums(p, v, tl, chunk * 32, tl.row0 + static_cast<int>(blockIdx.z) * kRowsCta + row, row & 31);
+__global__ void __launch_bounds__(kAddThreads) k_int8_dx_add(const __grid_constant__ Params p) {
+    Tile tl;
+    uint32_t sums[32];
+    if (add_parts<false>(p.q, kTileTok, &tl, sums))
+        store_sums(p, sums, tl, static_cast<int>(blockIdx.y) * 32,
+                   tl.row0 + static_cast<int>(blockIdx.z) * kRowsCta + static_cast<int>(threadIdx.x), threadIdx.x & 31);
 }
 
 // ------------------------------------------------------------------ host
@@ -459,36 +400,23 @@ int max_pairs() {
     return n;
 }
 
-// Most tiles of T rows, and the parts each is cut into: as many as give every
-// pair of SMs one, of at least kMinStages stages.  Adding them costs about 5 us
-// and 0.4 us a part, which a contraction of less than kMinSplit stages does not
-// earn and which ends at kMaxParts (256 x 5120 x 5120: 41 us whole, 30 in three
-// parts; 500 x 10000 x 128: 72 and 25).
-constexpr int kMinStages = 8, kMinSplit = 48, kMaxParts = 16;
-struct Split {
-    int64_t tiles;
-    int parts;
-};
-Split split_of(int64_t T, const Int8Weight& w) {
-    const int64_t pairs = num_sms() / 2 > 0 ? num_sms() / 2 : 1, kbt = ceil_div(w.N, kBK);
-    const int64_t tiles = w.E == 1 ? token_tiles(static_cast<int>(T), kTileTok) * ceil_div(w.K, kTileRows)
-                                   : int8_tiles(T, w.E, w.K, kTileTok);
-    int64_t parts = pairs / (tiles > 0 ? tiles : 1);
-    if (parts > kbt / kMinStages) parts = kbt / kMinStages;
-    if (parts > kMaxParts) parts = kMaxParts;
-    return Split{tiles, kbt < kMinSplit || parts < 2 ? 1 : static_cast<int>(parts)};
+// 256 x 5120 x 5120 takes 41 us in whole tiles and 30 in three parts, 500 x
+// 10000 x 128 72 and 28.
+Schedule schedule(const RowRanges& rr, const Int8Weight& w, int64_t* tiles) {
+    return schedule_of(rr, w.E, w.K, ceil_div(w.N, kBK), kTileTok, 32, tiles);
 }
-
-// Words of a part's slot: 256 rows of the widest tile.
-int64_t slot_words(int64_t T) { return static_cast<int64_t>(kTileRows) * (T < kTileTok ? round_up(T, 32) : kTileTok); }
 
 }  // namespace
 
-int int8_dx_narrow_parts(int64_t T, const Int8Weight& w) { return split_of(T, w).parts; }
+int int8_dx_narrow_parts(int64_t T, const Int8Weight& w) {
+    int64_t tiles;
+    return schedule(RowRanges{nullptr, T}, w, &tiles).parts;
+}
 
 size_t int8_dx_narrow_workspace(int64_t T, const Int8Weight& w) {
-    const Split sp = split_of(T, w);
-    return sp.parts == 1 ? 0 : static_cast<size_t>(sp.tiles * sp.parts * slot_words(T)) * 4;
+    int64_t tiles;
+    const Schedule q = schedule(RowRanges{nullptr, T}, w, &tiles);
+    return slots_bytes(q, tiles);
 }
 
 // dY: rows ldy (a multiple of 8) elements apart.
@@ -499,41 +427,29 @@ cudaError_t launch_int8_dx_narrow(const uint16_t* dY, int64_t ldy, const Int8Wei
     if (e != cudaSuccess) return e;
     const int most = max_pairs();
     if (most <= 0) return cudaErrorNotSupported;
-    const Split sp = split_of(rr.T, w);
+    int64_t tiles;
     Params p{};
     p.scale = w.scale;
-    p.rr = rr;
-    p.E = w.E;
+    p.q = schedule(rr, w, &tiles);
+    p.q.slots = static_cast<uint32_t*>(ws);
     p.N = static_cast<int>(w.N);
     p.K = static_cast<int>(w.K);
-    p.num_w = static_cast<int>(ceil_div(w.K, kTileRows));
-    p.kbt = static_cast<int>(ceil_div(w.N, kBK));
-    p.parts = sp.parts;
     p.dX = dX;
-    p.slots = static_cast<float*>(ws);
-    p.slot_words = slot_words(rr.T);
     Maps maps;
     bool ok = make_map(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.K, w.E * w.N, w.ld, kRowsCta, kBK);
     for (int i = 0; i < kBoxes; ++i)
         ok = ok && make_map(&maps.y[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dY, w.N, rr.T, ldy * 2, kBK,
                             static_cast<uint32_t>(box_rows(i)));
     if (!ok) return cudaErrorInvalidValue;
-    const int64_t items = sp.tiles * sp.parts;
+    const int64_t items = tiles * p.q.parts;
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = pair_config(attr, static_cast<int>(items < most ? items : most), st);
     e = cudaLaunchKernelEx(&cfg, k_int8_dx_narrow, maps, p);
     note_launches(1);
-    if (e != cudaSuccess || sp.parts == 1) return e;
-    cudaLaunchConfig_t fin{};
+    if (e != cudaSuccess || p.q.parts == 1) return e;
     cudaLaunchAttribute dep[1];
-    dep[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    dep[0].val.programmaticStreamSerializationAllowed = 1;
-    fin.gridDim = dim3(static_cast<unsigned>(sp.tiles), static_cast<unsigned>(p.slot_words / kTileRows / 32), 2);
-    fin.blockDim = dim3(kRowsCta);
-    fin.stream = st;
-    fin.attrs = dep;
-    fin.numAttrs = 1;
-    e = cudaLaunchKernelEx(&fin, k_int8_dx_parts, p);
+    const cudaLaunchConfig_t add = add_config(dep, p.q, tiles, st);
+    e = cudaLaunchKernelEx(&add, k_int8_dx_add, p);
     note_launches(1);
     return e;
 }

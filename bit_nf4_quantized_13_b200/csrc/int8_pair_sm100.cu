@@ -64,10 +64,8 @@ constexpr uint16_t kPairMask = 0x3;
 struct Params {
     const float* xs;   // T token scales
     const float* ws;   // E x N channel scales
-    RowRanges rr;
-    int E, N;
-    int num_w;         // weight tiles of one expert
-    int kbt;           // stages of a tile
+    Schedule q;        // weight tiles: ceil(N / 256); stages: ceil(K / 128)
+    int N;
     void* out;
 };
 
@@ -88,16 +86,17 @@ struct Pipe {
     __device__ uint32_t sB(int s) const { return sA(s) + kABytes; }
 };
 
-__device__ void role_tma(const Pipe& P, const Params& p, const RowTable& tb, int units, const Maps& maps) {
+__device__ void role_tma(const Pipe& P, const Params& p, const RowTable& tb, int items, const Maps& maps) {
     int local = 0;
-    for (int u = P.pair; u < units; u += P.num_pairs) {
-        const Tile tl = tile_of(tb, p.E, p.num_w, kTileTok, u);
+    for (int it = P.pair; it < items; it += P.num_pairs) {
+        const Item x = item_of(p.q, tb, kTileTok, it);
+        const Tile& tl = x.tl;
         const int half = mma_tokens(tl.toks) / 2;
         const int box = box_index(half);
         const int wrow = tl.expert * p.N + tl.row0 + static_cast<int>(P.rank) * kRowsCta;
         const int xrow = tl.tok0 + static_cast<int>(P.rank) * half;
         const uint32_t tx = 2u * static_cast<uint32_t>(kABytes + box_rows(box) * kBK);
-        for (int kb = 0; kb < p.kbt; ++kb, ++local) {
+        for (int kb = x.kb0; kb < x.kb0 + x.stages; ++kb, ++local) {
             const int s = local % kStages;
             const uint32_t ph = static_cast<uint32_t>(local / kStages) & 1u;
             if (!mbar_wait(P.empty(s), ph ^ 1u, &g_int8_error)) return;
@@ -117,17 +116,17 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int lan
     return ok != 0;
 }
 
-__device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, int units) {
+__device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, int items) {
     const uint64_t a0 = sdesc_kmajor_sw128(P.sA(0)), b0 = sdesc_kmajor_sw128(P.sB(0));
     int s = 0, i = 0;
     uint32_t ph = 0;
-    for (int u = P.pair; u < units; u += P.num_pairs, ++i) {
-        const Tile tl = tile_of(tb, p.E, p.num_w, kTileTok, u);
+    for (int it = P.pair; it < items; it += P.num_pairs, ++i) {
+        const Item x = item_of(p.q, tb, kTileTok, it);
         const int b = i & 1;
-        const uint32_t idesc = idesc_i8(kRowsPair, mma_tokens(tl.toks));
+        const uint32_t idesc = idesc_i8(kRowsPair, mma_tokens(x.tl.toks));
         if (!mbar_wait(P.acc_empty(b), (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u, &g_int8_error)) return;
         tc_fence_after();
-        for (int kb = 0; kb < p.kbt; ++kb) {
+        for (int kb = 0; kb < x.stages; ++kb) {
             if (!mbar_wait(P.full(s), ph, &g_int8_error)) return;
             tc_fence_after();
             const uint64_t off = static_cast<uint64_t>(s) * (kStageBytes / 16);
@@ -175,14 +174,14 @@ __device__ __forceinline__ void store_chunk(const Params& p, const uint32_t (&ac
 }
 
 template <bool kF32>
-__device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb, int units, int warp, int lane) {
+__device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb, int items, int warp, int lane) {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     __shared__ __align__(16) float s_sx[kEpiWarps][kWarpChunks * 32];
     float* sx = s_sx[warp - 2];
     int i = 0;
-    for (int u = P.pair; u < units; u += P.num_pairs, ++i) {
-        const Tile tl = tile_of(tb, p.E, p.num_w, kTileTok, u);
+    for (int it = P.pair; it < items; it += P.num_pairs, ++i) {
+        const Tile tl = item_of(p.q, tb, kTileTok, it).tl;
         const int b = i & 1;
         const int chunks = mma_tokens(tl.toks) / 32;
         const int chan = tl.row0 + static_cast<int>(P.rank) * kRowsCta + quarter * 32 + lane;
@@ -202,7 +201,10 @@ __device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb
             uint32_t acc[32];
             tmem_ld_32x32b_x32(P.tmem + lane_base + static_cast<uint32_t>(b * kTileTok + c * 32), acc);
             tmem_wait_ld();
-            store_chunk<kF32>(p, acc, sx + (c / 2) * 32, tl, c * 32, chan, sw, lane);
+            if (p.q.parts == 1)
+                store_chunk<kF32>(p, acc, sx + (c / 2) * 32, tl, c * 32, chan, sw, lane);
+            else
+                slot_store(p.q, it, P.rank, c, quarter * 32 + lane, acc);
         }
         tc_fence_before();
         __syncwarp();
@@ -246,21 +248,21 @@ k_int8_gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Para
         tma_prefetch_desc(&maps.w);
         for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.x[i]);
     }
-    if (warp == 2) build_table(p.rr, p.E, p.num_w, kTileTok, tb, lane);
+    if (warp == 2) build_table(p.q.rr, p.q.E, p.q.num_w, kTileTok, tb, lane);
     tc_fence_before();
     __syncthreads();
     cluster_arrive();  // both CTAs' barriers are initialised before any remote arrive
     cluster_wait();
     tc_fence_after();
     P.tmem = *tmem_slot;
-    const int units = tb.tile0[p.E];
+    const int items = tb.tile0[p.q.E] * p.q.parts;
     grid_dependency_wait();  // the quantized tokens
     if (warp == 0) {
-        if (elect_one()) role_tma(P, p, tb, units, maps);
+        if (elect_one()) role_tma(P, p, tb, items, maps);
         __syncwarp();
     } else if (warp == 1) {
         if (P.rank == 0 && elect_one()) {
-            role_mma(P, p, tb, units);
+            role_mma(P, p, tb, items);
             // every pair MMA issued (also on an early exit) has completed
             // before the tensor memory can be freed
             tc_commit_pair_mc(P.drain(), 1);
@@ -268,8 +270,9 @@ k_int8_gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Para
         }
         __syncwarp();
     } else {
-        role_epilogue<kF32>(P, p, tb, units, warp, lane);
+        role_epilogue<kF32>(P, p, tb, items, warp, lane);
     }
+    grid_launch_dependents();  // the kernel that adds the parts
     tc_fence_before();
     __syncthreads();
     cluster_arrive();  // neither CTA frees its tensor memory or leaves while the pair may still use it
@@ -278,6 +281,20 @@ k_int8_gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Para
         tc_fence_after();
         tmem_dealloc_pair(P.tmem, kTmemCols);
     }
+}
+
+template <bool kF32>
+__global__ void __launch_bounds__(kAddThreads) k_int8_gemm_add(const __grid_constant__ Params p) {
+    __shared__ __align__(16) float s_sx[32];
+    const int tok = static_cast<int>(blockIdx.y) * 32, lane = threadIdx.x & 31;
+    Tile tl;
+    uint32_t sums[32];
+    if (!add_parts<true>(p.q, kTileTok, &tl, sums)) return;
+    if (threadIdx.x < 32) s_sx[lane] = tok + lane < tl.toks ? p.xs[tl.tok0 + tok + lane] : 0.0f;
+    __syncthreads();
+    const int chan = tl.row0 + static_cast<int>(blockIdx.z) * kRowsCta + static_cast<int>(threadIdx.x);
+    const float sw = chan < p.N ? __ldg(p.ws + static_cast<int64_t>(tl.expert) * p.N + chan) : 0.0f;
+    store_chunk<kF32>(p, sums, s_sx, tl, tok, chan, sw, lane);
 }
 
 // ------------------------------------------------------------------ host
@@ -339,11 +356,22 @@ cudaError_t launch_pair(const Maps& maps, const Params& p, int64_t tiles, cudaSt
     if (e != cudaSuccess) return e;
     const int most = max_pairs<kF32>();
     if (most <= 0) return cudaErrorNotSupported;
+    const int64_t items = tiles * p.q.parts;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = pair_config(attr, static_cast<int>(tiles < most ? tiles : most), st, dependent);
+    const cudaLaunchConfig_t cfg = pair_config(attr, static_cast<int>(items < most ? items : most), st, dependent);
     e = cudaLaunchKernelEx(&cfg, k_int8_gemm_pair<kF32>, maps, p);
     note_launches(1);
+    if (e != cudaSuccess || p.q.parts == 1) return e;
+    cudaLaunchAttribute dep[1];
+    const cudaLaunchConfig_t add = add_config(dep, p.q, tiles, st);
+    e = cudaLaunchKernelEx(&add, k_int8_gemm_add<kF32>, p);
+    note_launches(1);
     return e;
+}
+
+// 500 x 512 x 11008 takes 35 us in whole tiles and 24 in ten parts.
+Schedule schedule(const RowRanges& rr, const Int8Weight& w, int64_t* tiles) {
+    return schedule_of(rr, w.E, w.N, ceil_div(w.K, kBK), kTileTok, 48, tiles);
 }
 
 }  // namespace
@@ -357,22 +385,28 @@ bool int8_pair_supported(int64_t T, const Int8Weight& w) {
     return int8_tiles(T, w.E, w.N, kTileTok) * ceil_div(w.K, kBK) < (int64_t(1) << 31);
 }
 
+// Workspace: the parts' slots.
+size_t int8_pair_workspace(int64_t T, const Int8Weight& w) {
+    int64_t tiles;
+    const Schedule q = schedule(RowRanges{nullptr, T}, w, &tiles);
+    return slots_bytes(q, tiles);
+}
+
 cudaError_t launch_int8_fwd_pair(const int8_t* x_codes, const float* x_scale, const Int8Weight& w,
-                                 const RowRanges& rr, void* out, int out_dtype, cudaStream_t st, bool dependent) {
+                                 const RowRanges& rr, void* out, int out_dtype, void* ws, cudaStream_t st,
+                                 bool dependent) {
+    int64_t tiles;
     Params p{};
     p.xs = x_scale;
     p.ws = w.scale;
-    p.rr = rr;
-    p.E = w.E;
+    p.q = schedule(rr, w, &tiles);
+    p.q.slots = static_cast<uint32_t*>(ws);
     p.N = static_cast<int>(w.N);
-    p.num_w = static_cast<int>(ceil_div(w.N, kRowsPair));
-    p.kbt = static_cast<int>(ceil_div(w.K, kBK));
     p.out = out;
     Maps maps;
     bool ok = make_map_i8(&maps.w, w.codes, w.K, w.E * w.N, w.ld, kRowsCta);
     for (int i = 0; i < kBoxes; ++i) ok = ok && make_map_i8(&maps.x[i], x_codes, w.K, rr.T, w.ld, box_rows(i));
     if (!ok) return cudaErrorInvalidValue;
-    const int64_t tiles = int8_tiles(rr.T, w.E, w.N, kTileTok);
     return out_dtype == 0 ? launch_pair<true>(maps, p, tiles, st, dependent)
                           : launch_pair<false>(maps, p, tiles, st, dependent);
 }

@@ -5,6 +5,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "sm100.cuh"
 
 namespace qlora {
 
@@ -97,6 +98,132 @@ __device__ __forceinline__ Tile tile_of(const RowTable& tb, int E, int num_w, in
     s.tok0 = lo + t * width;
     s.toks = min(width, hi - s.tok0);
     return s;
+}
+
+// A schedule: every tile, or (where the tiles leave most pairs of SMs idle: few
+// of them, with a long contraction) each tile's stages cut into `parts` runs
+// for as many pairs.  A part leaves its sums in a workspace slot of its own and
+// a second kernel adds them in order, so no pair waits for another and the
+// result does not depend on the order of arrival.
+struct Schedule {
+    RowRanges rr;
+    int E;
+    int num_w;           // weight-side tiles of one expert
+    int kbt;             // stages of a tile
+    int parts;           // parts of a tile
+    uint32_t* slots;     // parts > 1: a slot for each part
+    int64_t slot_words;  // 256 rows of the widest tile's tokens
+};
+
+// One part of a tile.
+struct Item {
+    Tile tl;
+    int kb0, stages;
+};
+
+__device__ __forceinline__ Item item_of(const Schedule& q, const RowTable& tb, int cap, int it) {
+    Item x;
+    int tile = it;
+    x.kb0 = 0;
+    x.stages = q.kbt;
+    if (q.parts > 1) {
+        tile = it / q.parts;
+        const int part = it - tile * q.parts;
+        x.kb0 = part * q.kbt / q.parts;
+        x.stages = (part + 1) * q.kbt / q.parts - x.kb0;
+    }
+    x.tl = tile_of(tb, q.E, q.num_w, cap, tile);
+    return x;
+}
+
+// A slot holds [CTA][chunk of 32 tokens][group of 4 tokens][row][4], so that
+// each lane's 16 bytes of a group are part of 512 contiguous ones.
+__device__ __forceinline__ uint4* slot_at(const Schedule& q, int slot, uint32_t rank, int chunk, int group, int row) {
+    return reinterpret_cast<uint4*>(q.slots + slot * q.slot_words + rank * (q.slot_words / 2) +
+                                    (static_cast<int64_t>(chunk * 8 + group) * (kTileRows / 2) + row) * 4);
+}
+
+__device__ __forceinline__ void slot_store(const Schedule& q, int slot, uint32_t rank, int chunk, int row,
+                                           const uint32_t (&v)[32]) {
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+        *slot_at(q, slot, rank, chunk, g, row) = make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+}
+
+// The adding kernel's block (tile, chunk of 32 tokens, CTA) of kAddThreads, a
+// row each: the tile and the row's sums over the parts (kInt: integers, else
+// fp32); false where the tile has no such chunk.
+constexpr int kAddThreads = kTileRows / 2;
+template <bool kInt>
+__device__ __forceinline__ bool add_parts(const Schedule& q, int cap, Tile* tl, uint32_t (&v)[32]) {
+    __shared__ int s_table[kRowTableBytes / 4];
+    const RowTable tb = row_table(s_table);
+    if (threadIdx.x < 32) build_table(q.rr, q.E, q.num_w, cap, tb, static_cast<int>(threadIdx.x));
+    __syncthreads();
+    const int tile = static_cast<int>(blockIdx.x), chunk = static_cast<int>(blockIdx.y);
+    sm100::grid_dependency_wait();  // the parts' sums
+    if (tile >= tb.tile0[q.E]) return false;
+    *tl = tile_of(tb, q.E, q.num_w, cap, tile);
+    if (chunk * 32 >= tl->toks) return false;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0u;  // the bits of 0.0f too
+#pragma unroll 2
+    for (int j = 0; j < q.parts; ++j) {
+        uint4 x[8];
+#pragma unroll
+        for (int g = 0; g < 8; ++g)
+            x[g] = __ldcg(slot_at(q, tile * q.parts + j, blockIdx.z, chunk, g, static_cast<int>(threadIdx.x)));
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            const uint32_t y[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t& a = v[4 * g + i];
+                a = kInt ? a + y[i] : __float_as_uint(__uint_as_float(a) + __uint_as_float(y[i]));
+            }
+        }
+    }
+    return true;
+}
+
+// The most tiles of a problem, and the parts each is cut into: as many as give
+// every pair of SMs one, of at least kMinStages stages, if that takes
+// `min_saved` stages off a pair's work.  Adding them costs about 5 us and 0.4
+// us a part, so they end at kMaxParts.
+constexpr int kMinStages = 8, kMaxParts = 16;
+inline Schedule schedule_of(const RowRanges& rr, int E, int64_t w_rows, int64_t kbt, int cap, int min_saved,
+                            int64_t* tiles) {
+    Schedule q{};
+    q.rr = rr;
+    q.E = E;
+    q.num_w = static_cast<int>(ceil_div(w_rows, kTileRows));
+    q.kbt = static_cast<int>(kbt);
+    q.slot_words = static_cast<int64_t>(kTileRows) * (rr.T < cap ? round_up(rr.T, 32) : cap);
+    *tiles = E == 1 ? static_cast<int64_t>(token_tiles(static_cast<int>(rr.T), cap)) * q.num_w
+                    : int8_tiles(rr.T, E, w_rows, cap);
+    const int64_t pairs = num_sms() / 2 > 0 ? num_sms() / 2 : 1;
+    int64_t parts = pairs / (*tiles > 0 ? *tiles : 1);
+    if (parts > kbt / kMinStages) parts = kbt / kMinStages;
+    if (parts > kMaxParts) parts = kMaxParts;
+    q.parts = parts > 1 && kbt - kbt / parts >= min_saved ? static_cast<int>(parts) : 1;
+    return q;
+}
+inline size_t slots_bytes(const Schedule& q, int64_t tiles) {
+    return q.parts == 1 ? 0 : static_cast<size_t>(tiles * q.parts * q.slot_words) * 4;
+}
+
+// The adding kernel's launch, dependent on the product's.
+inline cudaLaunchConfig_t add_config(cudaLaunchAttribute (&attr)[1], const Schedule& q, int64_t tiles,
+                                     cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(q.slot_words / kTileRows / 32), 2);
+    cfg.blockDim = dim3(kAddThreads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
 }
 
 // The MMA's width for a tile's tokens, and the token rows each CTA of the

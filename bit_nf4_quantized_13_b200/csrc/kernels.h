@@ -75,7 +75,9 @@ __device__ __forceinline__ void expert_rows(const RowRanges& rr, int e, int* lo,
 int64_t int8_tiles(int64_t T, int E, int64_t w_rows, int tile_tok);
 bool int8_pair_supported(int64_t T, const Int8Weight& w);
 cudaError_t launch_int8_fwd_pair(const int8_t* x_codes, const float* x_scale, const Int8Weight& w,
-                                 const RowRanges& rr, void* out, int out_dtype, cudaStream_t stream, bool dependent);
+                                 const RowRanges& rr, void* out, int out_dtype, void* ws, cudaStream_t stream,
+                                 bool dependent);
+size_t int8_pair_workspace(int64_t T, const Int8Weight& w);
 int int8_device_error(int reset);
 
 // int8_gemv.cu -- the forward for a few tokens, by streaming the weights.

@@ -378,8 +378,10 @@ int qlora_int8_quantize_rows(const void* x, int x_dtype, int64_t rows, int64_t K
  * The sum is exact (32-bit integers); out is fp32 (out_dtype 0) or bf16 bits
  * (out_dtype 1).  Y: M x N.
  */
+size_t qlora_int8_matmul_workspace_size(int64_t M, int64_t N, int64_t K);
 int qlora_int8_matmul(const int8_t* x_codes, const float* x_scale, int64_t M, int64_t N, int64_t K,
-                      const int8_t* w_codes, const float* w_scale, void* Y, int out_dtype, void* stream);
+                      const int8_t* w_codes, const float* w_scale, void* Y, int out_dtype, void* ws,
+                      size_t ws_bytes, void* stream);
 
 /*
  * qlora_int8_linear_fwd -- the tokens X (M x K bf16) quantized by row, then
@@ -417,9 +419,10 @@ size_t qlora_int8_expert_fwd_workspace_size(int64_t T, int E, int64_t N, int64_t
 int qlora_int8_expert_fwd(const uint16_t* X, const int32_t* offsets, int64_t T, int E, int64_t N, int64_t K,
                           const int8_t* w_codes, const float* w_scale, void* Y, int out_dtype, void* ws,
                           size_t ws_bytes, void* stream);
+size_t qlora_int8_expert_matmul_workspace_size(int64_t T, int E, int64_t N, int64_t K);
 int qlora_int8_expert_matmul(const int8_t* x_codes, const float* x_scale, const int32_t* offsets, int64_t T, int E,
                              int64_t N, int64_t K, const int8_t* w_codes, const float* w_scale, void* Y,
-                             int out_dtype, void* stream);
+                             int out_dtype, void* ws, size_t ws_bytes, void* stream);
 size_t qlora_int8_expert_bwd_workspace_size(int64_t T, int E, int64_t N, int64_t K);
 int qlora_int8_expert_bwd(const uint16_t* dY, const int32_t* offsets, int64_t T, int E, int64_t N, int64_t K,
                           const int8_t* w_codes, const float* w_scale, uint16_t* dX, void* ws, size_t ws_bytes,

@@ -100,7 +100,8 @@ def test_rows_nonfinite_are_marked_alone(K, dtype):
 FWD_SIZES = [(1, 1, 1), (1, 64, 64), (1, 5120, 512), (2, 33, 100), (3, 16, 4096), (7, 257, 1111), (8, 1000, 64),
              (9, 100, 5000), (15, 31, 48), (16, 512, 5120), (17, 130, 96), (31, 64, 1024), (33, 1003, 1111),
              (64, 300, 640), (100, 128, 3), (128, 256, 128), (130, 4097, 192), (255, 257, 129), (257, 512, 2048),
-             (300, 1024, 8200), (512, 640, 384), (700, 333, 777), (1025, 1280, 4096), (2049, 2304, 1024)]
+             (300, 1024, 8200), (512, 640, 384), (700, 333, 777), (1025, 1280, 4096), (2049, 2304, 1024), (300, 64, 11008), (40, 500, 9000),
+             (257, 260, 8200)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -223,6 +224,7 @@ EXPERT_CASES = [
     ([1500, 2600, 1025], 0, 0, 65, 513),
     ([5, 0, 30], 2, 1, 5000, 130),          # few tiles, a long contraction of the gradient
     ([300, 20], 0, 4, 4097, 64),
+    ([18, 0, 30], 1, 2, 100, 8300),         # and of the forward
 ]
 
 

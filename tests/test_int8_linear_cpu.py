@@ -37,7 +37,7 @@ def test_quantize_rows_refusals(lib):
 
 
 def test_linear_refusals(lib):
-    for f, x, ws in ((lib.qlora_int8_linear_fwd, (P,), (P, BIG)), (lib.qlora_int8_matmul, (P, P), ())):
+    for f, x, ws in ((lib.qlora_int8_linear_fwd, (P,), (P, BIG)), (lib.qlora_int8_matmul, (P, P), (P, BIG))):
         assert f(*x, -1, 8, 8, P, P, P, 1, *ws, None) == INVALID
         assert f(*x, 4, 0, 8, P, P, P, 1, *ws, None) == INVALID
         assert f(*x, 4, 8, 0, P, P, P, 1, *ws, None) == INVALID
@@ -50,7 +50,8 @@ def test_linear_refusals(lib):
         assert f(*x, 4, 8, 8, P, P + 4, P, 1, *ws, None) == INVALID
         assert f(*x, 4, 8, 8, P, P, None, 1, *ws, None) == INVALID
         assert f(*(None,) * len(x), 4, 8, 8, P, P, P, 1, *ws, None) == INVALID
-        assert f(*(None,) * len(x), 0, 8, 8, P, P, None, 1, *((None, 0) if ws else ()), None) == OK  # no tokens
+        assert f(*(None,) * len(x), 0, 8, 8, P, P, None, 1, None, 0, None) == OK  # no tokens
+    assert lib.qlora_int8_matmul(P, P, 400, 64, 11008, P, P, P, 1, None, 0, None) == WORKSPACE  # a split contraction
     f = lib.qlora_int8_linear_fwd
     assert f(P, 400, 8, 8, P, P, P, 1, None, BIG, None) == WORKSPACE
     assert f(P, 400, 8, 8, P, P, P, 1, P + 8, BIG, None) == WORKSPACE
@@ -66,13 +67,13 @@ def test_linear_refusals(lib):
 
 
 def test_expert_refusals(lib):
-    for f, x, ws in ((lib.qlora_int8_expert_fwd, (P,), (P, BIG)), (lib.qlora_int8_expert_matmul, (P, P), ())):
+    for f, x, ws in ((lib.qlora_int8_expert_fwd, (P,), (P, BIG)), (lib.qlora_int8_expert_matmul, (P, P), (P, BIG))):
         assert f(*x, P, 4, 0, 8, 8, P, P, P, 1, *ws, None) == INVALID
         assert f(*x, P, 4, 1025, 8, 8, P, P, P, 1, *ws, None) == UNSUPPORTED
         assert f(*x, P, 4, 1024, 1 << 22, 8, P, P, P, 1, *ws, None) == UNSUPPORTED  # E N >= 2^31
         assert f(*x, None, 4, 2, 8, 8, P, P, P, 1, *ws, None) == INVALID            # no offsets
         assert f(*x, P + 4, 4, 2, 8, 8, P, P, P, 1, *ws, None) == INVALID
-        assert f(*x, None, 0, 2, 8, 8, P, P, None, 1, *((None, 0) if ws else ()), None) == OK
+        assert f(*x, None, 0, 2, 8, 8, P, P, None, 1, None, 0, None) == OK
     assert lib.qlora_int8_expert_fwd(P, P, 400, 2, 8, 8, P, P, P, 1, P, 0, None) == WORKSPACE
     f = lib.qlora_int8_expert_bwd
     assert f(P, None, 4, 2, 8, 8, P, P, P, P, BIG, None) == INVALID
@@ -87,8 +88,14 @@ def test_workspace_sizes(lib):
     assert q.qlora_int8_expert_fwd_workspace_size(100, 4, 8, 33) >= 100 * 48 + 400
     assert q.qlora_int8_linear_fwd_workspace_size(4, 8, 131073) == 0
     assert q.qlora_int8_expert_bwd_workspace_size(4, 1025, 8, 8) == 0
-    assert q.qlora_int8_linear_bwd_workspace_size(100, 64, 33) == 0
-    assert q.qlora_int8_linear_bwd_workspace_size(100, 33, 64) >= 100 * 40 * 2
+    assert q.qlora_int8_matmul_workspace_size(1, 64, 4096) == 0
+    assert q.qlora_int8_expert_matmul_workspace_size(400, 4, 8, 33) < q.qlora_int8_expert_fwd_workspace_size(400, 4, 8, 33)
+    assert q.qlora_int8_linear_bwd_workspace_size(100, 40, 64) == 0
+    assert q.qlora_int8_linear_bwd_workspace_size(100, 33, 64) >= 100 * 40 * 2  # padded rows of dY
+    # few tiles with a long contraction: the parts' sums
+    assert q.qlora_int8_linear_bwd_workspace_size(100, 8192, 64) >= 2 * 128 * 256 * 4
+    assert q.qlora_int8_matmul_workspace_size(100, 64, 11008) >= 2 * 128 * 256 * 4
+    assert q.qlora_int8_linear_bwd_workspace_size(0, 64, 64) == 0
     assert q.qlora_int8_linear_fwd_workspace_size(1, 64, 4096) == 0  # one kernel that quantizes its own token
 
 
