@@ -14,7 +14,7 @@
 // Warp roles (320 threads per CTA, persistent over the pair's tiles):
 //   warp 0     TMA producer (both CTAs, into their own shared memory; the
 //              bytes count on the even CTA's barrier): 128 bytes of
-//              contraction per stage, a ring of kStages
+//              contraction per stage, a ring of six to nine
 //   warp 1     MMA issuer (one thread of the even CTA)
 //   warps 2-9  epilogue: TMEM lane quarter w % 4 (32 output channels), every
 //              second 32-token column chunk; scales, rounding, stores
@@ -47,15 +47,14 @@ constexpr int kRowsPair = kTileRows;           // MMA M: 128 in each CTA
 static_assert(kRowsPair == 2 * kRowsCta, "a tile's rows are halved between the CTAs");
 constexpr int kTileTok = 256;                  // largest MMA N
 constexpr int kBK = 128;                       // contraction bytes per stage
-constexpr int kStages = 6;
 constexpr int kABytes = kRowsCta * kBK;        // 16 KiB
-constexpr int kBBytes = kTileTok / 2 * kBK;    // 16 KiB: half of the tokens in each CTA
-constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kRingBytes = 192 * 1024;
+constexpr int kMaxStages = 9;
 constexpr int kEpiWarps = 8;
 constexpr int kWarpChunks = kTileTok / 32 / 2;   // 32-token chunks of an epilogue warp
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr uint32_t kTmemCols = 512;
-constexpr int kBarOff = kStages * kStageBytes;
+constexpr int kBarOff = kRingBytes;
 constexpr int kTableOff = kBarOff + 256;
 constexpr int kSmemBytes = 1024 /* alignment slack */ + kTableOff + kRowTableBytes;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
@@ -66,8 +65,19 @@ struct Params {
     const float* ws;   // E x N channel scales
     Schedule q;        // weight tiles: ceil(N / 256); stages: ceil(K / 128)
     int N;
+    int cap;           // most tokens of a tile
+    int stages;        // of the ring
+    int stage_bytes;   // the weight's 16 KiB, then half of the tokens
     void* out;
 };
+
+// The ring for tiles of up to `cap` tokens (64, 128 or 256): the smaller the
+// tokens' part of a stage, the more stages are in flight, which is what the
+// weight stream of small tiles needs.
+__host__ __device__ constexpr int stage_bytes(int cap) { return kABytes + cap / 2 * kBK; }
+__host__ __device__ constexpr int ring_stages(int cap) { return kRingBytes / stage_bytes(cap); }
+static_assert(ring_stages(64) == kMaxStages && ring_stages(128) == 8 && ring_stages(kTileTok) == 6, "rings");
+static_assert(8 * (2 * kMaxStages + 5) + 4 <= kTableOff - kBarOff, "barriers and the TMEM address");
 
 struct Maps {
     CUtensorMap w;          // weight rows: boxes of kRowsCta
@@ -78,32 +88,34 @@ struct Pipe {
     uint32_t smem, bar0, tmem, rank;
     int pair, num_pairs;
     __device__ uint32_t full(int s) const { return bar0 + 8u * s; }
-    __device__ uint32_t empty(int s) const { return bar0 + 8u * (kStages + s); }
-    __device__ uint32_t acc_full(int b) const { return bar0 + 8u * (2 * kStages + b); }
-    __device__ uint32_t acc_empty(int b) const { return bar0 + 8u * (2 * kStages + 2 + b); }
-    __device__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + 4); }
-    __device__ uint32_t sA(int s) const { return smem + static_cast<uint32_t>(s * kStageBytes); }
-    __device__ uint32_t sB(int s) const { return sA(s) + kABytes; }
+    __device__ uint32_t empty(int s) const { return bar0 + 8u * (kMaxStages + s); }
+    __device__ uint32_t acc_full(int b) const { return bar0 + 8u * (2 * kMaxStages + b); }
+    __device__ uint32_t acc_empty(int b) const { return bar0 + 8u * (2 * kMaxStages + 2 + b); }
+    __device__ uint32_t drain() const { return bar0 + 8u * (2 * kMaxStages + 4); }
 };
 
 __device__ void role_tma(const Pipe& P, const Params& p, const RowTable& tb, int items, const Maps& maps) {
-    int local = 0;
+    int s = 0;
+    uint32_t ph = 1;
     for (int it = P.pair; it < items; it += P.num_pairs) {
-        const Item x = item_of(p.q, tb, kTileTok, it);
+        const Item x = item_of(p.q, tb, p.cap, it);
         const Tile& tl = x.tl;
         const int half = mma_tokens(tl.toks) / 2;
         const int box = box_index(half);
         const int wrow = tl.expert * p.N + tl.row0 + static_cast<int>(P.rank) * kRowsCta;
         const int xrow = tl.tok0 + static_cast<int>(P.rank) * half;
         const uint32_t tx = 2u * static_cast<uint32_t>(kABytes + box_rows(box) * kBK);
-        for (int kb = x.kb0; kb < x.kb0 + x.stages; ++kb, ++local) {
-            const int s = local % kStages;
-            const uint32_t ph = static_cast<uint32_t>(local / kStages) & 1u;
-            if (!mbar_wait(P.empty(s), ph ^ 1u, &g_int8_error)) return;
+        for (int kb = x.kb0; kb < x.kb0 + x.stages; ++kb) {
+            if (!mbar_wait(P.empty(s), ph, &g_int8_error)) return;
             const uint32_t bar = cluster_map(P.full(s), 0);
             if (P.rank == 0) mbar_arrive_expect_tx(P.full(s), tx);
-            tma_load_2d_pair(P.sA(s), &maps.w, bar, kb * kBK, wrow);
-            tma_load_2d_pair(P.sB(s), &maps.x[box], bar, kb * kBK, xrow);
+            const uint32_t stage = P.smem + static_cast<uint32_t>(s * p.stage_bytes);
+            tma_load_2d_pair(stage, &maps.w, bar, kb * kBK, wrow);
+            tma_load_2d_pair(stage + kABytes, &maps.x[box], bar, kb * kBK, xrow);
+            if (++s == p.stages) {
+                s = 0;
+                ph ^= 1u;
+            }
         }
     }
 }
@@ -117,11 +129,11 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int lan
 }
 
 __device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, int items) {
-    const uint64_t a0 = sdesc_kmajor_sw128(P.sA(0)), b0 = sdesc_kmajor_sw128(P.sB(0));
+    const uint64_t a0 = sdesc_kmajor_sw128(P.smem), b0 = sdesc_kmajor_sw128(P.smem + kABytes);
     int s = 0, i = 0;
     uint32_t ph = 0;
     for (int it = P.pair; it < items; it += P.num_pairs, ++i) {
-        const Item x = item_of(p.q, tb, kTileTok, it);
+        const Item x = item_of(p.q, tb, p.cap, it);
         const int b = i & 1;
         const uint32_t idesc = idesc_i8(kRowsPair, mma_tokens(x.tl.toks));
         if (!mbar_wait(P.acc_empty(b), (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u, &g_int8_error)) return;
@@ -129,13 +141,13 @@ __device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, int
         for (int kb = 0; kb < x.stages; ++kb) {
             if (!mbar_wait(P.full(s), ph, &g_int8_error)) return;
             tc_fence_after();
-            const uint64_t off = static_cast<uint64_t>(s) * (kStageBytes / 16);
+            const uint64_t off = static_cast<uint64_t>(s) * static_cast<uint64_t>(p.stage_bytes / 16);
 #pragma unroll
             for (int kk = 0; kk < kBK / 32; ++kk)  // 32 bytes along a row: 2 descriptor units
                 mma_i8_ss_pair(P.tmem + b * kTileTok, a0 + off + 2 * kk, b0 + off + 2 * kk, idesc,
                                     (kb > 0 || kk > 0) ? 1u : 0u);
             tc_commit_pair_mc(P.empty(s), kPairMask);
-            if (++s == kStages) {
+            if (++s == p.stages) {
                 s = 0;
                 ph ^= 1u;
             }
@@ -181,7 +193,7 @@ __device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb
     float* sx = s_sx[warp - 2];
     int i = 0;
     for (int it = P.pair; it < items; it += P.num_pairs, ++i) {
-        const Tile tl = item_of(p.q, tb, kTileTok, it).tl;
+        const Tile tl = item_of(p.q, tb, p.cap, it).tl;
         const int b = i & 1;
         const int chunks = mma_tokens(tl.toks) / 32;
         const int chan = tl.row0 + static_cast<int>(P.rank) * kRowsCta + quarter * 32 + lane;
@@ -218,7 +230,7 @@ k_int8_gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Para
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 5);
     const RowTable tb = row_table(smem + kTableOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -229,7 +241,7 @@ k_int8_gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Para
     P.pair = static_cast<int>(blockIdx.x >> 1);
     P.num_pairs = static_cast<int>(gridDim.x >> 1);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < p.stages; ++s) {
             mbar_init(P.full(s), 1);   // the even CTA's expect_tx arrival (+ both CTAs' bytes)
             mbar_init(P.empty(s), 1);  // the pair MMA's commit
         }
@@ -248,7 +260,7 @@ k_int8_gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Para
         tma_prefetch_desc(&maps.w);
         for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.x[i]);
     }
-    if (warp == 2) build_table(p.q.rr, p.q.E, p.q.num_w, kTileTok, tb, lane);
+    if (warp == 2) build_table(p.q.rr, p.q.E, p.q.num_w, p.cap, tb, lane);
     tc_fence_before();
     __syncthreads();
     cluster_arrive();  // both CTAs' barriers are initialised before any remote arrive
@@ -289,7 +301,7 @@ __global__ void __launch_bounds__(kAddThreads) k_int8_gemm_add(const __grid_cons
     const int tok = static_cast<int>(blockIdx.y) * 32, lane = threadIdx.x & 31;
     Tile tl;
     uint32_t sums[32];
-    if (!add_parts<true>(p.q, kTileTok, &tl, sums)) return;
+    if (!add_parts<true>(p.q, p.cap, &tl, sums)) return;
     if (threadIdx.x < 32) s_sx[lane] = tok + lane < tl.toks ? p.xs[tl.tok0 + tok + lane] : 0.0f;
     __syncthreads();
     const int chan = tl.row0 + static_cast<int>(blockIdx.z) * kRowsCta + static_cast<int>(threadIdx.x);
@@ -369,9 +381,16 @@ cudaError_t launch_pair(const Maps& maps, const Params& p, int64_t tiles, cudaSt
     return e;
 }
 
+// The most tokens of a tile.  Dense: the batch decides.  Experts: their average
+// rows do (an expert with more takes its weight through the L2 once a tile).
+int tile_cap(int64_t T, const Int8Weight& w) {
+    const int64_t m = ceil_div(T, T < w.E ? T : w.E);
+    return m <= 64 ? 64 : m <= 128 ? 128 : kTileTok;
+}
+
 // 500 x 512 x 11008 takes 35 us in whole tiles and 24 in ten parts.
 Schedule schedule(const RowRanges& rr, const Int8Weight& w, int64_t* tiles) {
-    return schedule_of(rr, w.E, w.N, ceil_div(w.K, kBK), kTileTok, 48, tiles);
+    return schedule_of(rr, w.E, w.N, ceil_div(w.K, kBK), tile_cap(rr.T, w), 48, tiles);
 }
 
 }  // namespace
@@ -382,7 +401,7 @@ int64_t int8_tiles(int64_t T, int E, int64_t w_rows, int tile_tok) {
 }
 
 bool int8_pair_supported(int64_t T, const Int8Weight& w) {
-    return int8_tiles(T, w.E, w.N, kTileTok) * ceil_div(w.K, kBK) < (int64_t(1) << 31);
+    return int8_tiles(T, w.E, w.N, tile_cap(T, w)) * ceil_div(w.K, kBK) < (int64_t(1) << 31);
 }
 
 // Workspace: the parts' slots.
@@ -401,6 +420,9 @@ cudaError_t launch_int8_fwd_pair(const int8_t* x_codes, const float* x_scale, co
     p.ws = w.scale;
     p.q = schedule(rr, w, &tiles);
     p.q.slots = static_cast<uint32_t*>(ws);
+    p.cap = tile_cap(rr.T, w);
+    p.stages = ring_stages(p.cap);
+    p.stage_bytes = stage_bytes(p.cap);
     p.N = static_cast<int>(w.N);
     p.out = out;
     Maps maps;
