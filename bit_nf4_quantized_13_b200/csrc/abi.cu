@@ -389,7 +389,7 @@ int check_int8(int64_t T, int E, int64_t N, int64_t K, bool by_expert, const int
     if (T < 0 || E < 1 || N < 1 || K < 1) return QLORA_ERR_INVALID_ARG;
     if (by_expert && T > 0 && !ok_ptr(offsets)) return QLORA_ERR_INVALID_ARG;
     if (K > QLORA_INT8_MAX_K || E > QLORA_MAX_EXPERTS || T >= (int64_t(1) << 30) || N >= (int64_t(1) << 30) ||
-        E * N >= (int64_t(1) << 31))
+        E * N > (int64_t(1) << 31) - 512)  // a tile's copies may start up to 256 rows behind the last
         return QLORA_ERR_UNSUPPORTED;
     return QLORA_OK;
 }

@@ -13,8 +13,8 @@
 // consecutive codes of channels g and g + 8, which are the A fragments of two
 // mma.m16n8k32 (the contraction index is permuted the same way in both
 // operands, so no code moves between lanes); a warp reads 64 bytes of each of
-// 16 rows per two instructions and keeps two halves of four such loads in
-// flight, across steps too.  Integer sums are exact, so the warps' partial
+// 16 rows per two instructions and keeps eight such loads in flight, across
+// steps too (sixteen were no faster).  Integer sums are exact, so the warps' partial
 // sums may be added in any order: through shared memory, once a step.  Two
 // blocks an SM (117 registers, no spills) stream as fast as three or four and
 // leave room for the token fragments; giving each warp whole steps, to have
@@ -84,7 +84,7 @@ __device__ __forceinline__ RowVec<uint16_t> load_token(const GemvParams& p, int 
     return v;
 }
 
-// NT tiles of 8 tokens at a time.
+// T <= 8 NT tokens.
 template <int NT, bool kFused, bool kF32>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 k_int8_gemv(const GemvParams p) {
@@ -164,9 +164,8 @@ k_int8_gemv(const GemvParams p) {
             open_step();
         }
     };
-    HalfUnit h0, h1;
-    const bool works = warp < nunits;
-    if (works) {
+    HalfUnit h0, h1;  // the next unit
+    if (warp < nunits) {
         open_step();
         load_half(h0, 0);
         load_half(h1, 1);
@@ -200,68 +199,55 @@ k_int8_gemv(const GemvParams p) {
     for (int step = static_cast<int>(blockIdx.x); step < steps; step += static_cast<int>(gridDim.x)) {
         const int e = dense ? 0 : s_active[step / p.groups];
         const int n0 = (dense ? step : step % p.groups) * kRows;
-        int lo, hi;
+        int lo, hi;  // at most T <= 8 NT rows
         expert_rows(p.rr, e, &lo, &hi);
-        for (int m0 = lo; m0 < hi; m0 += 8 * NT) {
-            const bool again = m0 + 8 * NT < hi;  // the weights are needed once more (from L2)
-            int acc[NT][4] = {};
-            auto multiply = [&](const HalfUnit& h, int k) {
+        int acc[NT][4] = {};
+        auto multiply = [&](const HalfUnit& half, int k) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int kk = k + 64 * i + 16 * t;
-                    const uint4 a = h.v[2 * i], b = h.v[2 * i + 1];
+            for (int i = 0; i < 2; ++i) {
+                const int kk = k + 64 * i + 16 * t;
+                const uint4 a = half.v[2 * i], b = half.v[2 * i + 1];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const int m = m0 + 8 * nt + g;
-                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                        if (m < hi && kk < ld)
-                            x = *reinterpret_cast<const uint4*>(kFused ? s_x + m * (ld + kXPad) + kk
-                                                                       : p.xc + m * ld + kk);
-                        mma_s8(acc[nt], a.x, b.x, a.y, b.y, x.x, x.y);
-                        mma_s8(acc[nt], a.z, b.z, a.w, b.w, x.z, x.w);
-                    }
-                }
-            };
-            if (works) {
-                for (int u = warp; u < nunits; u += kWarps) {
-                    const int k = u * kUnit;
-                    if (again && u + kWarps >= nunits) {  // the loads start this step over
-                        l_step = step;
-                        l_unit = warp;
-                        open_step();
-                    }
-                    multiply(h0, k);
-                    load_half(h0, 0);
-                    multiply(h1, k + kHalf);
-                    load_half(h1, 1);
-                    advance();
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int m = lo + 8 * nt + g;
+                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                    if (m < hi && kk < ld)
+                        x = *reinterpret_cast<const uint4*>(kFused ? s_x + m * (ld + kXPad) + kk : p.xc + m * ld + kk);
+                    mma_s8(acc[nt], a.x, b.x, a.y, b.y, x.x, x.y);
+                    mma_s8(acc[nt], a.z, b.z, a.w, b.w, x.z, x.w);
                 }
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                *reinterpret_cast<int2*>(&s_sum[warp][g][8 * nt + 2 * t]) = make_int2(acc[nt][0], acc[nt][1]);
-                *reinterpret_cast<int2*>(&s_sum[warp][g + 8][8 * nt + 2 * t]) = make_int2(acc[nt][2], acc[nt][3]);
-            }
-            __syncthreads();
-            for (int i = threadIdx.x; i < kRows * 8 * NT; i += kThreads) {
-                const int r = i % kRows, col = i / kRows;
-                const int m = m0 + col, n = n0 + r;
-                if (m < hi && n < p.w.N) {
-                    int sum = 0;
-#pragma unroll
-                    for (int wv = 0; wv < kWarps; ++wv) sum += s_sum[wv][r][col];
-                    const float sx = kFused ? s_scale[m] : p.xs[m];
-                    const float sw = __ldg(p.w.scale + static_cast<int64_t>(e) * p.w.N + n);
-                    const float v = __fmul_rn(__fmul_rn(__int2float_rn(sum), sx), sw);
-                    const int64_t o = static_cast<int64_t>(m) * p.w.N + n;
-                    if (kF32)
-                        static_cast<float*>(p.out)[o] = v;
-                    else
-                        static_cast<uint16_t*>(p.out)[o] = f32_to_bf16_bits(v);
-                }
-            }
-            __syncthreads();
+        };
+        for (int u = warp; u < nunits; u += kWarps) {
+            multiply(h0, u * kUnit);
+            load_half(h0, 0);
+            multiply(h1, u * kUnit + kHalf);
+            load_half(h1, 1);
+            advance();
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            *reinterpret_cast<int2*>(&s_sum[warp][g][8 * nt + 2 * t]) = make_int2(acc[nt][0], acc[nt][1]);
+            *reinterpret_cast<int2*>(&s_sum[warp][g + 8][8 * nt + 2 * t]) = make_int2(acc[nt][2], acc[nt][3]);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < kRows * 8 * NT; i += kThreads) {
+            const int r = i % kRows, m = lo + i / kRows, n = n0 + r;
+            if (m < hi && n < p.w.N) {
+                int sum = 0;
+#pragma unroll
+                for (int wv = 0; wv < kWarps; ++wv) sum += s_sum[wv][r][i / kRows];
+                const float sx = kFused ? s_scale[m] : p.xs[m];
+                const float sw = __ldg(p.w.scale + static_cast<int64_t>(e) * p.w.N + n);
+                const float v = __fmul_rn(__fmul_rn(__int2float_rn(sum), sx), sw);
+                const int64_t o = static_cast<int64_t>(m) * p.w.N + n;
+                if (kF32)
+                    static_cast<float*>(p.out)[o] = v;
+                else
+                    static_cast<uint16_t*>(p.out)[o] = f32_to_bf16_bits(v);
+            }
+        }
+        __syncthreads();
     }
 }
 
