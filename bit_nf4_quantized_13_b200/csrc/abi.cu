@@ -354,9 +354,7 @@ int qlora_device_error(int reset) {
     const int b = lora_device_error(reset);
     const int c = gemv_device_error(reset);
     const int d = int8_device_error(reset);
-    int e = int8_dx_device_error(reset);
-    const int f = int8_dx_narrow_device_error(reset);
-    if (e == QLORA_OK) e = f;
+    const int e = int8_dx_device_error(reset);
     return a != QLORA_OK ? a : b != QLORA_OK ? b : c != QLORA_OK ? c : d != QLORA_OK ? d : e;
 }
 

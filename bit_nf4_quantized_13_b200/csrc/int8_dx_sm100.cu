@@ -6,26 +6,37 @@
 // computed transposed, D[k][m] += W'^T[k][n] * dY[m][n], with the weight as
 // the MMA's A operand (MN-major: a row of the staged tile holds consecutive k
 // of one n), so the codes are read in their natural row-major layout.  A tile
-// is 256 columns k (128 in each CTA of the pair) x up to 512 tokens, held as
-// one or two accumulators of 256: a converted weight tile then feeds 512
-// tokens, which keeps the shared-memory traffic (16 KiB converted, 32 KiB of
-// dY copied, 64 KiB read by the MMAs per 1024 MMA cycles) under its 128 bytes
-// a cycle.  As in the forward, the MMA's N follows the tokens of a ragged
-// tile, and a tile of up to 256 tokens uses one accumulator and leaves the
-// other to the next tile.
+// is 256 columns k (128 in each CTA of the pair) x up to 256 tokens; as in the
+// forward, the MMA's N follows the tokens of a ragged tile.
 //
-// Warp roles (576 threads per CTA, persistent over the pair's tiles):
-//   warp 0      TMA producer of dY (both CTAs, into their own shared memory;
-//               the bytes count on the even CTA's barrier)
-//   warp 1      MMA issuer (one thread of the even CTA)
-//   warps 2-17  converters: warp w takes the stages i with i % 4 ==
-//               (w - 2) / 4 (always ring slot i % 4), a quarter of the stage's
-//               64 x 128 codes; then the epilogue of its TMEM lane quarter
-// A warp's load instruction covers 64 consecutive codes of 8 rows; a lane
-// turns 16 codes of a row into two 16-byte pieces of the swizzled tile
-// without bank conflicts.  Conversion: a code, offset by 128, is placed in the
-// mantissa of 2^23 by a byte permute; one subtraction gives the exact value,
-// one multiplication RN32(code * scale), one packing conversion two bf16.
+// The conversion of the weights is the other half of the work, and of a tile
+// of few tokens nearly all of it: 64 x 128 codes per CTA for 4 MMAs.  Its warps
+// do nothing else (when they also loaded the codes through registers and wrote
+// the outputs, a stage of few tokens took 700 to 900 cycles instead of 475):
+//
+//   warp 0       copies dY's token halves (TMA, bytes on the even CTA's barrier)
+//   warp 1       issues the MMAs (one thread of the even CTA)
+//   warp 2       copies the codes (TMA) into a ring of kRaw stages of 8 KiB
+//   warps 4-19   converters: warp w takes the stages i with i % 4 == (w - 4) / 4,
+//                a quarter of the stage's 64 x 128 codes, from shared memory
+//                into the swizzled bf16 tile
+//   warps 20-23  epilogue of the TMEM lane quarter w % 4, under the next tile's
+//                stages (two accumulators)
+//
+// At 256 tokens a stage's shared-memory traffic (48 KiB copied or converted,
+// 40 KiB read) bounds it at about 700 cycles where its MMAs take 512.  A tile
+// of 512 tokens with four-fold less conversion per MMA, its codes loaded
+// through registers, took the same time or more on every shape but one
+// (4096 x 11008 x 4096: 248 against 245 us; 2048 x 4096 x 4096: 57 against 61).
+//
+// Conversion: a code, offset by 128, is placed in the mantissa of 2^23 by a
+// byte permute; one subtraction gives the exact value, one multiplication
+// RN32(code * scale), one packing conversion two bf16 (convert4).
+//
+// The copied codes are swizzled too (16-byte piece ^ row % 8).  A lane's row in
+// a group of 8 is chosen so that the two rows of each 8 lanes differ in bit 2
+// (the load of 4 neighbouring pieces) and in bit 0 (the store of every second
+// piece): neither has bank conflicts.
 //
 // Every mbarrier wait is bounded; a timeout records QLORA_ERR_TIMEOUT in a
 // sticky device word and ends the role.
@@ -45,36 +56,37 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kRowsCta = kTileRows / 2;             // columns k per CTA
-constexpr int kSubTok = 256;                        // largest MMA N: tokens of an accumulator
-constexpr int kSubs = 2;
-constexpr int kTileTok = kSubs * kSubTok;
-constexpr int kBK = 64;                             // contraction (n) per stage
+constexpr int kRowsCta = kTileRows / 2;   // columns k per CTA
+constexpr int kTileTok = 256;             // largest MMA N
+constexpr int kBK = 64;                   // contraction (n) per stage
 constexpr int kStages = 4;
-constexpr int kPanelBytes = kBK * 128;              // 64 n x 64 k bf16
-constexpr int kABytes = 2 * kPanelBytes;            // 16 KiB
-constexpr int kBHalfBytes = kSubTok / 2 * kBK * 2;  // 16 KiB: half of an accumulator's tokens
-constexpr int kStageBytes = kABytes + kSubs * kBHalfBytes;
-constexpr int kConvWarps = 16;
+constexpr int kPanelBytes = kBK * 128;    // 64 n x 64 k bf16
+constexpr int kABytes = 2 * kPanelBytes;  // 16 KiB
+constexpr int kBBytes = kTileTok / 2 * kBK * 2;  // 16 KiB: half of the tokens
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kRaw = 10;
+constexpr int kRawBytes = kBK * kRowsCta;  // 8 KiB of codes
+constexpr int kConvWarp0 = 4, kConvWarps = 16, kEpiWarp0 = kConvWarp0 + kConvWarps;
 constexpr int kParts = kConvWarps / 4;
 static_assert(kParts == kStages, "a part's stages must always use the same ring slot");
-constexpr int kThreads = 32 * (2 + kConvWarps);
+constexpr int kThreads = 32 * (kEpiWarp0 + 4);
 constexpr uint32_t kTmemCols = 512;
-constexpr int kBarOff = kStages * kStageBytes;
-constexpr int kTableOff = kBarOff + 256;
+constexpr int kRawOff = kStages * kStageBytes;
+constexpr int kBarOff = kRawOff + kRaw * kRawBytes;
+constexpr int kTableOff = kBarOff + 512;
 constexpr int kSmemBytes = 1024 /* alignment slack */ + kTableOff + kRowTableBytes;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 constexpr uint16_t kPairMask = 0x3;
 
 struct Params {
-    Int8Weight w;
-    RowRanges rr;
-    int num_w;      // column tiles: ceil(K / 256)
-    int kbt;        // stages of a tile: ceil(N / 64)
+    const float* scale;  // E x N
+    Schedule q;          // column tiles: ceil(K / 256); stages: ceil(N / 64)
+    int N, K;
     uint16_t* dX;
 };
 
 struct Maps {
+    CUtensorMap w;          // codes: boxes of 64 n x 128 k
     CUtensorMap y[kBoxes];  // dY rows: boxes of box_rows(i) x 64 columns
 };
 
@@ -84,42 +96,56 @@ struct Pipe {
     __device__ uint32_t full_b(int s) const { return bar0 + 8u * s; }
     __device__ uint32_t full_a(int s) const { return bar0 + 8u * (kStages + s); }
     __device__ uint32_t empty(int s) const { return bar0 + 8u * (2 * kStages + s); }
-    __device__ uint32_t acc_full(int b) const { return bar0 + 8u * (3 * kStages + b); }
-    __device__ uint32_t acc_empty(int b) const { return bar0 + 8u * (3 * kStages + 2 + b); }
-    __device__ uint32_t drain() const { return bar0 + 8u * (3 * kStages + 4); }
+    __device__ uint32_t raw_full(int s) const { return bar0 + 8u * (3 * kStages + s); }
+    __device__ uint32_t raw_empty(int s) const { return bar0 + 8u * (3 * kStages + kRaw + s); }
+    __device__ uint32_t acc_full(int b) const { return bar0 + 8u * (3 * kStages + 2 * kRaw + b); }
+    __device__ uint32_t acc_empty(int b) const { return bar0 + 8u * (3 * kStages + 2 * kRaw + 2 + b); }
+    __device__ uint32_t drain() const { return bar0 + 8u * (3 * kStages + 2 * kRaw + 4); }
     __device__ uint32_t sA(int s) const { return smem + static_cast<uint32_t>(s * kStageBytes); }
-    __device__ uint32_t sB(int s, int sub) const { return sA(s) + kABytes + sub * kBHalfBytes; }
+    __device__ uint32_t sRaw(int s) const { return smem + static_cast<uint32_t>(kRawOff + s * kRawBytes); }
+};
+constexpr int kBars = 3 * kStages + 2 * kRaw + 5;
+static_assert(8 * kBars + 8 <= kTableOff - kBarOff, "barriers and the TMEM address");
+
+// A position in a ring of kSlots, with the parity of its turn.
+template <int kSlots>
+struct Ring {
+    int slot;
+    uint32_t turn;
+    __device__ void step(int n) {
+        slot += n;
+        if (slot >= kSlots) {
+            slot -= kSlots;
+            turn ^= 1u;
+        }
+    }
 };
 
-// Tokens of accumulator `sub` of a tile.
-__device__ __forceinline__ int sub_tokens(const Tile& tl, int sub) {
-    return min(max(tl.toks - sub * kSubTok, 0), kSubTok);
+__device__ void role_tokens(const Pipe& P, const Params& p, const RowTable& tb, const Items& items, const Maps& maps) {
+    Ring<kStages> ring{0, 1};
+    for (int it = P.pair; it < items.count; it += P.num_pairs) {
+        const Item x = item_of(p.q, tb, items, kTileTok, it);
+        const Tile& tl = x.tl;
+        const int half = mma_tokens(tl.toks) / 2, box = box_index(half);
+        const int row = tl.tok0 + static_cast<int>(P.rank) * half;
+        const uint32_t tx = 2u * static_cast<uint32_t>(box_rows(box) * kBK * 2);
+        for (int kb = x.kb0; kb < x.kb0 + x.stages; ++kb, ring.step(1)) {
+            if (!mbar_wait(P.empty(ring.slot), ring.turn, &g_int8_dx_error)) return;
+            if (P.rank == 0) mbar_arrive_expect_tx(P.full_b(ring.slot), tx);
+            tma_load_2d_pair(P.sA(ring.slot) + kABytes, &maps.y[box], cluster_map(P.full_b(ring.slot), 0), kb * kBK, row);
+        }
+    }
 }
 
-__device__ void role_tma(const Pipe& P, const Params& p, const RowTable& tb, int units, const Maps& maps) {
-    int local = 0;
-    for (int u = P.pair; u < units; u += P.num_pairs) {
-        const Tile tl = tile_of(tb, p.w.E, p.num_w, kTileTok, u);
-        int box[kSubs], row[kSubs];
-        uint32_t tx = 0;
-        int subs = 0;
-        for (int sub = 0; sub < kSubs; ++sub) {
-            const int n = sub_tokens(tl, sub);
-            if (n == 0) break;
-            const int half = mma_tokens(n) / 2;
-            box[sub] = box_index(half);
-            row[sub] = tl.tok0 + sub * kSubTok + static_cast<int>(P.rank) * half;
-            tx += 2u * static_cast<uint32_t>(box_rows(box[sub]) * kBK * 2);
-            ++subs;
-        }
-        for (int kb = 0; kb < p.kbt; ++kb, ++local) {
-            const int s = local % kStages;
-            const uint32_t ph = static_cast<uint32_t>(local / kStages) & 1u;
-            if (!mbar_wait(P.empty(s), ph ^ 1u, &g_int8_dx_error)) return;
-            const uint32_t bar = cluster_map(P.full_b(s), 0);
-            if (P.rank == 0) mbar_arrive_expect_tx(P.full_b(s), tx);
-            for (int sub = 0; sub < subs; ++sub)
-                tma_load_2d_pair(P.sB(s, sub), &maps.y[box[sub]], bar, kb * kBK, row[sub]);
+__device__ void role_codes(const Pipe& P, const Params& p, const RowTable& tb, const Items& items, const Maps& maps) {
+    Ring<kRaw> ring{0, 1};
+    for (int it = P.pair; it < items.count; it += P.num_pairs) {
+        const Item x = item_of(p.q, tb, items, kTileTok, it);
+        const int col = x.tl.row0 + static_cast<int>(P.rank) * kRowsCta, n0 = x.tl.expert * p.N;
+        for (int kb = x.kb0; kb < x.kb0 + x.stages; ++kb, ring.step(1)) {
+            if (!mbar_wait(P.raw_empty(ring.slot), ring.turn, &g_int8_dx_error)) return;
+            mbar_arrive_expect_tx(P.raw_full(ring.slot), kRawBytes);
+            tma_load_2d(P.sRaw(ring.slot), &maps.w, P.raw_full(ring.slot), col, n0 + kb * kBK);
         }
     }
 }
@@ -129,189 +155,128 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, &g_int8_dx_error));
 }
 
-// Accumulators are taken in turn: the g-th one used is columns (g & 1) * 256,
-// for the (g >> 1)-th time.
-__device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, int units) {
-    const uint64_t a0 = sdesc_mnmajor_sw128(P.sA(0), kPanelBytes), b0 = sdesc_kmajor_sw128(P.sB(0, 0));
-    int s = 0, g = 0;
-    uint32_t ph = 0;
-    for (int u = P.pair; u < units; u += P.num_pairs) {
-        const Tile tl = tile_of(tb, p.w.E, p.num_w, kTileTok, u);
-        const int subs = tl.toks > kSubTok ? 2 : 1;
-        const uint32_t idesc0 = idesc_bf16(kTileRows, mma_tokens(sub_tokens(tl, 0)), 1, 0);
-        const uint32_t idesc1 = idesc_bf16(kTileRows, mma_tokens(sub_tokens(tl, 1)), 1, 0);
-        for (int a = g; a < g + subs; ++a)
-            if (!mbar_wait(P.acc_empty(a & 1), (static_cast<uint32_t>(a >> 1) & 1u) ^ 1u, &g_int8_dx_error)) return;
+// The pair's i-th item uses accumulator i & 1 (columns (i & 1) * 256).
+__device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, const Items& items) {
+    const uint64_t a0 = sdesc_mnmajor_sw128(P.sA(0), kPanelBytes), b0 = sdesc_kmajor_sw128(P.sA(0) + kABytes);
+    Ring<kStages> ring{0, 0};
+    int i = 0;
+    for (int it = P.pair; it < items.count; it += P.num_pairs, ++i) {
+        const Item x = item_of(p.q, tb, items, kTileTok, it);
+        const uint32_t idesc = idesc_bf16(kTileRows, mma_tokens(x.tl.toks), 1, 0);
+        const int b = i & 1;
+        if (!mbar_wait(P.acc_empty(b), (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u, &g_int8_dx_error)) return;
         tc_fence_after();
-        const uint32_t d0 = P.tmem + (g & 1) * kSubTok, d1 = P.tmem + ((g + 1) & 1) * kSubTok;
-        for (int kb = 0; kb < p.kbt; ++kb) {
-            if (!mbar_wait(P.full_b(s), ph, &g_int8_dx_error)) return;
-            if (!mbar_wait(P.full_a(s), ph, &g_int8_dx_error)) return;
+        for (int kb = 0; kb < x.stages; ++kb, ring.step(1)) {
+            if (!mbar_wait(P.full_b(ring.slot), ring.turn, &g_int8_dx_error)) return;
+            if (!mbar_wait(P.full_a(ring.slot), ring.turn, &g_int8_dx_error)) return;
             tc_fence_after();
-            const uint64_t off = static_cast<uint64_t>(s) * (kStageBytes / 16);
+            const uint64_t off = static_cast<uint64_t>(ring.slot) * (kStageBytes / 16);
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {
-                const uint64_t ad = a0 + off + kk * (2048 / 16);  // 16 rows of 128 bytes
-                const uint64_t bd = b0 + off + kk * 2;            // 32 bytes along a row
-                const uint32_t more = (kb > 0 || kk > 0) ? 1u : 0u;
-                mma_bf16_ss_pair(d0, ad, bd, idesc0, more);
-                if (subs == 2) mma_bf16_ss_pair(d1, ad, bd + kBHalfBytes / 16, idesc1, more);
-            }
-            tc_commit_pair_mc(P.empty(s), kPairMask);
-            if (++s == kStages) {
-                s = 0;
-                ph ^= 1u;
-            }
+            for (int kk = 0; kk < kBK / 16; ++kk)  // A: 16 rows of 128 bytes; B: 32 bytes along a row
+                mma_bf16_ss_pair(P.tmem + b * kTileTok, a0 + off + kk * (2048 / 16), b0 + off + kk * 2, idesc,
+                                 (kb > 0 || kk > 0) ? 1u : 0u);
+            tc_commit_pair_mc(P.empty(ring.slot), kPairMask);
         }
-        for (int sub = 0; sub < subs; ++sub, ++g) tc_commit_pair_mc(P.acc_full(g & 1), kPairMask);
+        tc_commit_pair_mc(P.acc_full(b), kPairMask);
     }
 }
 
-__device__ __forceinline__ uint4 ldg_codes(const int8_t* p) {
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// Outputs of the tile `tl`, whose accumulators are the g-th and following:
-// this warp's TMEM lane quarter, every fourth 32-token chunk.
-__device__ __forceinline__ bool tile_epilogue(const Pipe& P, const Params& p, const Tile& tl, int& g, int part,
-                                              int quarter, int lane) {
-    const int subs = tl.toks > kSubTok ? 2 : 1;
-    const int col = tl.row0 + static_cast<int>(P.rank) * kRowsCta + quarter * 32 + lane;
+__device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb, const Items& items, int cwarp, int lane) {
+    const int quarter = cwarp & 3, part = cwarp >> 2;
+    const int panel = quarter >> 1;                 // which 64 of this CTA's 128 columns
+    const int c = lane & 3;                         // 16-code piece of the 64
+    const int q = lane >> 3;
+    const int r = (lane & 4) ? q ^ 5 : q;           // row within 8
+    const int row0 = (quarter & 1) * 32 + r;        // + 8 j: this lane's rows of the stage
+    const uint32_t full_a0 = cluster_map(P.full_a(part), 0);
+    const uint32_t src0 = static_cast<uint32_t>(row0 * 128 + (((panel * 4 + c) ^ r) << 4));
+    const uint32_t dst = P.sA(part) + static_cast<uint32_t>(panel * kPanelBytes + row0 * 128);
+    const uint32_t dst0 = dst + (((2 * c) ^ r) << 4), dst1 = dst + (((2 * c + 1) ^ r) << 4);
+    Ring<kRaw> raw{part, 0};
+    uint32_t turn = 1;
+    int kb = part;  // this part's next stage, counted from the item's first
+    for (int it = P.pair; it < items.count; it += P.num_pairs) {
+        const Item x = item_of(p.q, tb, items, kTileTok, it);
+        const float* scale = p.scale + static_cast<int64_t>(x.tl.expert) * p.N;
+        for (; kb < x.stages; kb += kParts) {
+            // rows past N hold other codes or zeros: scale 0 makes them 0
+            const int n = (x.kb0 + kb) * kBK + (quarter & 1) * 32 + lane;
+            const float mine = n < p.N ? __ldg(scale + n) : 0.0f;
+            if (!warp_wait(P.raw_full(raw.slot), raw.turn)) return;
+            const uint32_t src = P.sRaw(raw.slot) + src0;
+            uint4 cb[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) cb[j] = lds_v4(src + j * 1024);
+            uint32_t v[32];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float sc = __shfl_sync(0xffffffffu, mine, 8 * j + r);
+                const uint64_t ms = (static_cast<uint64_t>(__float_as_uint(sc)) << 32) | __float_as_uint(sc);
+                const uint32_t w4[4] = {cb[j].x, cb[j].y, cb[j].z, cb[j].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) convert4(w4[i], ms, v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+            }
+            __syncwarp();  // every lane has its codes
+            if (lane == 0) mbar_arrive(P.raw_empty(raw.slot));
+            raw.step(kParts);
+            if (!warp_wait(P.empty(part), turn)) return;
+            turn ^= 1u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst0 + j * 1024), "r"(v[8 * j]),
+                             "r"(v[8 * j + 1]), "r"(v[8 * j + 2]), "r"(v[8 * j + 3])
+                             : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst1 + j * 1024), "r"(v[8 * j + 4]),
+                             "r"(v[8 * j + 5]), "r"(v[8 * j + 6]), "r"(v[8 * j + 7])
+                             : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(full_a0);
+        }
+        kb -= x.stages;
+    }
+}
+
+// This thread's 32 sums (tokens tok .. of column `col`) to dX.
+__device__ __forceinline__ void store_sums(const Params& p, const uint32_t (&sums)[32], const Tile& tl, int tok,
+                                           int col, int lane) {
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(sums[j]);
+    store_bf16_chunk(p.dX + static_cast<int64_t>(tl.tok0 + tok) * p.K, p.K, col, tl.toks - tok, v, lane);
+}
+
+__device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb, const Items& items, int quarter, int lane) {
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const int K = static_cast<int>(p.w.K);
-    for (int sub = 0; sub < subs; ++sub, ++g) {
-        const int b = g & 1;
-        const int toks = sub_tokens(tl, sub);
-        if (!warp_wait(P.acc_full(b), static_cast<uint32_t>(g >> 1) & 1u)) return false;
+    int i = 0;
+    for (int it = P.pair; it < items.count; it += P.num_pairs, ++i) {
+        const Item x = item_of(p.q, tb, items, kTileTok, it);
+        const int b = i & 1, row = quarter * 32 + lane;
+        if (!warp_wait(P.acc_full(b), static_cast<uint32_t>(i >> 1) & 1u)) return;
         tc_fence_after();
 #pragma unroll 1
-        for (int c = part; c * 32 < toks; c += kParts) {
+        for (int tok = 0; tok < x.tl.toks; tok += 32) {
             uint32_t acc[32];
-            tmem_ld_32x32b_x32(P.tmem + lane_base + static_cast<uint32_t>(b * kSubTok + c * 32), acc);
+            tmem_ld_32x32b_x32(P.tmem + lane_base + static_cast<uint32_t>(b * kTileTok + tok), acc);
             tmem_wait_ld();
-            float v[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(acc[j]);
-            const int tok = sub * kSubTok + c * 32;
-            store_bf16_chunk(p.dX + static_cast<int64_t>(tl.tok0 + tok) * K, K, col, tl.toks - tok, v, lane);
+            if (x.slot < 0)
+                store_sums(p, acc, x.tl, tok, x.tl.row0 + static_cast<int>(P.rank) * kRowsCta + row, lane);
+            else
+                slot_store(p.q, x.slot, P.rank, tok / 32, row, acc);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(cluster_map(P.acc_empty(b), 0));
-    }
-    return true;
-}
-
-__device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb, int units, int warp, int lane) {
-    const int quarter = warp & 3;
-    const int part = (warp - 2) >> 2;
-    const int panel = quarter >> 1;                // which 64 of this CTA's 128 columns
-    const int r = lane >> 2, c = lane & 3;         // row within 8, 16-code piece of the 64
-    const uint32_t full_a0 = cluster_map(P.full_a(part), 0);
-    const int tiles = P.pair < units ? (units - P.pair + P.num_pairs - 1) / P.num_pairs : 0;
-    const int ld = static_cast<int>(p.w.ld), N = static_cast<int>(p.w.N);
-    const uint32_t dst = P.sA(part) + static_cast<uint32_t>(panel * kPanelBytes);
-
-    // the cursor of the code loads: stage l_kb of this pair's tile l_tile
-    int l_tile = 0, l_kb = part;
-    const int8_t* l_codes = nullptr;  // row 0 of the tile's expert, this lane's first column
-    const float* l_scale = nullptr;
-    bool l_in = false;                // the column is inside the padded row
-    auto open_tile = [&]() {          // moves l_kb into its tile
-        while (l_kb >= p.kbt) {
-            l_kb -= p.kbt;
-            ++l_tile;
-        }
-        if (l_tile >= tiles) return;
-        const Tile tl = tile_of(tb, p.w.E, p.num_w, kTileTok, P.pair + l_tile * P.num_pairs);
-        const int k = tl.row0 + static_cast<int>(P.rank) * kRowsCta + panel * 64 + c * 16;
-        l_codes = p.w.codes + static_cast<int64_t>(tl.expert) * N * ld + k;
-        l_scale = p.w.scale + static_cast<int64_t>(tl.expert) * N;
-        l_in = k < ld;
-    };
-    uint4 cb[4];
-    float sc[4];
-    const int64_t ld8 = static_cast<int64_t>(8) * ld;
-    auto issue = [&]() {  // loads the cursor's stage and moves the cursor to this part's next one
-        if (l_tile >= tiles) return;
-        const int n0 = l_kb * kBK + (quarter & 1) * 32;  // the quarter's first row
-        const int8_t* src = l_codes + static_cast<int64_t>(n0 + r) * ld;
-        const float* scale = l_scale + n0 + r;
-        if (l_in && n0 + 32 <= N) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                cb[j] = ldg_codes(src + j * ld8);
-                sc[j] = __ldg(scale + 8 * j);
-            }
-            // this part's next stage but one of the same tile, towards L2: the
-            // loads above are only one of this part's stages ahead
-            if (c == 0 && n0 + 2 * kStages * kBK + 32 <= N) {
-                const int8_t* far = src + static_cast<int64_t>(2 * kStages * kBK) * ld;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) prefetch_l2(far + j * ld8);
-            }
-        } else {  // rows past N are zero (they are part of the contraction)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool ok = l_in && n0 + r + 8 * j < N;
-                cb[j] = ok ? ldg_codes(src + j * ld8) : make_uint4(0u, 0u, 0u, 0u);
-                sc[j] = ok ? __ldg(scale + 8 * j) : 0.0f;
-            }
-        }
-        l_kb += kStages;
-        if (l_kb >= p.kbt) open_tile();
-    };
-
-    int next_epi = 0, g = 0;  // the next tile whose outputs this warp writes
-    open_tile();
-    issue();
-    uint32_t ph = 1;
-    int tile = 0, kb = part;  // the stage being converted
-    for (;; kb += kStages) {
-        for (; kb >= p.kbt; kb -= p.kbt) ++tile;
-        if (tile >= tiles) break;
-        uint32_t v[32];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t w4[4] = {cb[j].x, cb[j].y, cb[j].z, cb[j].w};
-            const uint64_t ms = (static_cast<uint64_t>(__float_as_uint(sc[j])) << 32) | __float_as_uint(sc[j]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) convert4(w4[i], ms, v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
-        }
-        if (!warp_wait(P.empty(part), ph)) return;
-        ph ^= 1u;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int row = (quarter & 1) * 32 + 8 * j + r;  // row & 7 == r
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                 dst + static_cast<uint32_t>(row * 128 + (((2 * c + h) ^ r) << 4))),
-                             "r"(v[8 * j + 4 * h]), "r"(v[8 * j + 4 * h + 1]), "r"(v[8 * j + 4 * h + 2]),
-                             "r"(v[8 * j + 4 * h + 3])
-                             : "memory");
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(full_a0);
-        // the tiles before this stage's are complete or about to be: write
-        // them now, with the next tile's first stages already converted
-        while (next_epi < tile) {
-            const Tile tl = tile_of(tb, p.w.E, p.num_w, kTileTok, P.pair + next_epi * P.num_pairs);
-            if (!tile_epilogue(P, p, tl, g, part, quarter, lane)) return;
-            ++next_epi;
-        }
-        issue();
-    }
-    while (next_epi < tiles) {
-        const Tile tl = tile_of(tb, p.w.E, p.num_w, kTileTok, P.pair + next_epi * P.num_pairs);
-        if (!tile_epilogue(P, p, tl, g, part, quarter, lane)) return;
-        ++next_epi;
     }
 }
 
@@ -320,7 +285,7 @@ k_int8_dx_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kStages + 5);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
     const RowTable tb = row_table(smem + kTableOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -336,9 +301,13 @@ k_int8_dx_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params
             mbar_init(P.full_a(s), 2 * 4);  // the part's four warps in each CTA
             mbar_init(P.empty(s), 1);       // the pair MMA's commit
         }
+        for (int s = 0; s < kRaw; ++s) {
+            mbar_init(P.raw_full(s), 1);    // this CTA's expect_tx arrival (+ its bytes)
+            mbar_init(P.raw_empty(s), 4);   // the part's four warps
+        }
         for (int b = 0; b < 2; ++b) {
             mbar_init(P.acc_full(b), 1);
-            mbar_init(P.acc_empty(b), 2 * kConvWarps);
+            mbar_init(P.acc_empty(b), 2 * 4);
         }
         mbar_init(P.drain(), 1);
         fence_barrier_init();
@@ -347,31 +316,38 @@ k_int8_dx_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params
         tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish_pair();
     }
-    if (warp == 1 && lane == 0)
+    if (warp == 1 && lane == 0) {
+        tma_prefetch_desc(&maps.w);
         for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.y[i]);
-    if (warp == 2) build_table(p.rr, p.w.E, p.num_w, kTileTok, tb, lane);
+    }
+    if (warp == 2) build_table(p.q.rr, p.q.E, p.q.num_w, kTileTok, tb, lane);
     tc_fence_before();
     __syncthreads();
     cluster_arrive();  // both CTAs' barriers are initialised before any remote arrive
     cluster_wait();
     tc_fence_after();
     P.tmem = *tmem_slot;
-    const int units = tb.tile0[p.w.E];
+    const Items items = items_of(p.q, tb);
+    grid_dependency_wait();  // dY's padded rows
     if (warp == 0) {
-        if (elect_one()) role_tma(P, p, tb, units, maps);
-        __syncwarp();
+        if (elect_one()) role_tokens(P, p, tb, items, maps);
     } else if (warp == 1) {
         if (P.rank == 0 && elect_one()) {
-            role_mma(P, p, tb, units);
+            role_mma(P, p, tb, items);
             // every pair MMA issued (also on an early exit) has completed
             // before the tensor memory can be freed
             tc_commit_pair_mc(P.drain(), 1);
             mbar_wait(P.drain(), 0u, &g_int8_dx_error);
         }
-        __syncwarp();
-    } else {
-        role_convert(P, p, tb, units, warp, lane);
+    } else if (warp == 2) {
+        if (elect_one()) role_codes(P, p, tb, items, maps);
+    } else if (warp >= kEpiWarp0) {
+        role_epilogue(P, p, tb, items, warp & 3, lane);
+    } else if (warp >= kConvWarp0) {
+        role_convert(P, p, tb, items, warp - kConvWarp0, lane);
     }
+    __syncwarp();
+    grid_launch_dependents();  // the kernel that adds the parts
     tc_fence_before();
     __syncthreads();
     cluster_arrive();  // neither CTA frees its tensor memory or leaves while the pair may still use it
@@ -382,39 +358,53 @@ k_int8_dx_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params
     }
 }
 
+__global__ void __launch_bounds__(kAddThreads) k_int8_dx_add(const __grid_constant__ Params p) {
+    Tile tl;
+    uint32_t sums[32];
+    if (add_parts<false>(p.q, kTileTok, &tl, sums))
+        store_sums(p, sums, tl, static_cast<int>(blockIdx.y) * 32,
+                   tl.row0 + static_cast<int>(blockIdx.z) * kRowsCta + static_cast<int>(threadIdx.x), threadIdx.x & 31);
+}
+
 // Rows of dY whose length is not a multiple of 8 (a copy's row stride is a
 // multiple of 16 bytes), into rows of `ld` elements.
 __global__ void __launch_bounds__(256) k_pad_rows(const uint16_t* __restrict__ src, int64_t rows, int n, int ld,
                                                   uint16_t* __restrict__ dst) {
+    grid_launch_dependents();
     for (int64_t m = blockIdx.x; m < rows; m += gridDim.x)
         for (int i = threadIdx.x; i < n; i += 256) dst[m * ld + i] = src[m * n + i];
 }
 
 // ------------------------------------------------------------------ host
-bool make_map_dy(CUtensorMap* m, const void* base, int64_t N, int64_t rows, int64_t ld, uint32_t box) {
+// A row-major matrix of `rows` rows, `stride` bytes apart, of `inner`
+// elements; 128-byte swizzled boxes of box_inner x box_rows, zero fill outside.
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t inner, int64_t rows, int64_t stride,
+              uint32_t box_inner, uint32_t box_outer) {
     auto fn = tensor_map_encoder();
     if (!fn) return false;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-    cuuint32_t boxes[2] = {kBK, box};
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+    cuuint32_t box[2] = {box_inner, box_outer};
     cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaLaunchConfig_t pair_config(cudaLaunchAttribute (&attr)[1], int pairs, cudaStream_t st) {
+cudaLaunchConfig_t pair_config(cudaLaunchAttribute (&attr)[2], int pairs, cudaStream_t st, bool dependent) {
     cudaLaunchConfig_t cfg{};
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(2 * static_cast<unsigned>(pairs));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = dependent ? 2 : 1;
     return cfg;
 }
 
@@ -424,8 +414,8 @@ int max_pairs() {
     if (!current_context_id(&ctx)) return 0;
     int n = 0;
     memo.get(ctx, &n, [](int* v) {
-        cudaLaunchAttribute attr[1];
-        const cudaLaunchConfig_t cfg = pair_config(attr, num_sms(), nullptr);
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg = pair_config(attr, num_sms(), nullptr, false);
         int c = 0;
         if (cudaOccupancyMaxActiveClusters(&c, k_int8_dx_pair, &cfg) != cudaSuccess) {
             cudaGetLastError();
@@ -437,77 +427,66 @@ int max_pairs() {
     return n;
 }
 
-// The most tokens of a tile: kTileTok (this kernel) or kSubTok (the narrow
-// one).  Dense: the fewer cycles, by the measured cost of 64 n of a tile (this
-// kernel 2.1 a token, 800 at least; the narrow one 2.8, 475 at least) times
-// the rounds of tiles.  512 x 5120 x 5120 takes 61 us here and 41 there, 4096 x
-// 11008 x 4096 246 and 266.  Experts: ragged rows fill wide tiles badly and
-// level out better in small ones (eight experts of 11008 x 4096 with 57 to 1540
-// of 4096 rows: 334 and 309 us), so wide tiles are left to experts of 1024 rows
-// and more on average.
-int tile_cap(int64_t T, const Int8Weight& w) {
-    if (w.E > 1) return T < 1024 * static_cast<int64_t>(w.E) ? kSubTok : kTileTok;
-    const int64_t pairs = num_sms() / 2 > 0 ? num_sms() / 2 : 1;
-    const int m = static_cast<int>(T);
-    auto rounds = [&](int cap) { return ceil_div(token_tiles(m, cap) * ceil_div(w.K, kTileRows), pairs); };
-    auto cost = [&](int cap, int tenths, int least) {
-        const int c = token_width(m, cap) * tenths / 10;
-        return c > least ? c : least;
-    };
-    const int64_t narrow = rounds(kSubTok) * cost(kSubTok, 28, 475) / int8_dx_narrow_parts(T, w);
-    return narrow <= rounds(kTileTok) * cost(kTileTok, 21, 800) ? kSubTok : kTileTok;
+// 256 x 5120 x 5120 takes 41 us in whole tiles and 30 in three parts, 500 x
+// 10000 x 128 72 and 28.
+Schedule schedule(const RowRanges& rr, const Int8Weight& w) {
+    return schedule_of(rr, w.E, w.K, ceil_div(w.N, kBK), kTileTok, 32, sm_pairs());
+}
+
+// Workspace: dY's rows padded to 16 bytes, where N is not a multiple of 8, then
+// the parts' slots.
+size_t padded_bytes(int64_t T, const Int8Weight& w) {
+    return w.N % 8 == 0 ? 0 : static_cast<size_t>(round_up(T * round_up(w.N, 8) * 2, 256));
+}
+size_t parts_bytes(int64_t T, const Int8Weight& w) {
+    return slots_bytes(schedule(RowRanges{nullptr, T}, w), kTileTok);
 }
 
 }  // namespace
 
 bool int8_dx_supported(int64_t T, const Int8Weight& w) {
-    return int8_tiles(T, w.E, w.K, kSubTok) * ceil_div(w.N, kBK) < (int64_t(1) << 31);
+    return int8_tiles(T, w.E, w.K, kTileTok) * ceil_div(w.N, kBK) < (int64_t(1) << 31);
 }
 
-// Workspace: dY's rows padded to 16 bytes, where N is not a multiple of 8, then
-// the narrow kernel's.
-size_t dx_padded_bytes(int64_t T, const Int8Weight& w) {
-    return w.N % 8 == 0 ? 0 : static_cast<size_t>(round_up(T * round_up(w.N, 8) * 2, 256));
-}
-
-size_t int8_dx_workspace(int64_t T, const Int8Weight& w) {
-    return dx_padded_bytes(T, w) + (tile_cap(T, w) == kSubTok ? int8_dx_narrow_workspace(T, w) : 0);
-}
+size_t int8_dx_workspace(int64_t T, const Int8Weight& w) { return padded_bytes(T, w) + parts_bytes(T, w); }
 
 cudaError_t launch_int8_dx(const uint16_t* dY, const Int8Weight& w, const RowRanges& rr, uint16_t* dX, void* ws,
                            cudaStream_t st) {
-    cudaError_t e;
-    const int64_t ld = round_up(w.N, 8);
-    if (ld != w.N) {
+    static ContextMemo<int> attr_memo;
+    cudaError_t e = ensure_smem_limit(attr_memo, k_int8_dx_pair, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (max_pairs() < 1) return cudaErrorNotSupported;
+    const int64_t ldy = round_up(w.N, 8);
+    if (ldy != w.N) {
         const int64_t cap = static_cast<int64_t>(num_sms()) * 8;
         k_pad_rows<<<static_cast<unsigned>(rr.T < cap ? rr.T : cap), 256, 0, st>>>(
-            dY, rr.T, static_cast<int>(w.N), static_cast<int>(ld), static_cast<uint16_t*>(ws));
+            dY, rr.T, static_cast<int>(w.N), static_cast<int>(ldy), static_cast<uint16_t*>(ws));
         note_launches(1);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         dY = static_cast<const uint16_t*>(ws);
     }
-    if (tile_cap(rr.T, w) == kSubTok)
-        return launch_int8_dx_narrow(dY, ld, w, rr, dX, static_cast<char*>(ws) + dx_padded_bytes(rr.T, w), st);
-    static ContextMemo<int> attr_memo;
-    e = ensure_smem_limit(attr_memo, k_int8_dx_pair, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    const int most = max_pairs();
-    if (most <= 0) return cudaErrorNotSupported;
     Params p{};
-    p.w = w;
-    p.rr = rr;
-    p.num_w = static_cast<int>(ceil_div(w.K, kTileRows));
-    p.kbt = static_cast<int>(ceil_div(w.N, kBK));
+    p.scale = w.scale;
+    p.q = schedule(rr, w);
+    if (parts_bytes(rr.T, w) > 0) p.q.slots = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + padded_bytes(rr.T, w));
+    p.N = static_cast<int>(w.N);
+    p.K = static_cast<int>(w.K);
     p.dX = dX;
     Maps maps;
-    bool ok = true;
-    for (int i = 0; i < kBoxes; ++i) ok = ok && make_map_dy(&maps.y[i], dY, w.N, rr.T, ld, box_rows(i));
+    bool ok = make_map(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.K, w.E * w.N, w.ld, kRowsCta, kBK);
+    for (int i = 0; i < kBoxes; ++i)
+        ok = ok && make_map(&maps.y[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dY, w.N, rr.T, ldy * 2, kBK,
+                            static_cast<uint32_t>(box_rows(i)));
     if (!ok) return cudaErrorInvalidValue;
-    const int64_t tiles = int8_tiles(rr.T, w.E, w.K, kTileTok);
-    cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = pair_config(attr, static_cast<int>(tiles < most ? tiles : most), st);
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = pair_config(attr, p.q.pairs, st, ldy != w.N);
     e = cudaLaunchKernelEx(&cfg, k_int8_dx_pair, maps, p);
+    note_launches(1);
+    if (e != cudaSuccess || !p.q.slots) return e;
+    cudaLaunchAttribute dep[1];
+    const cudaLaunchConfig_t add = add_config(dep, p.q, st);
+    e = cudaLaunchKernelEx(&add, k_int8_dx_add, p);
     note_launches(1);
     return e;
 }

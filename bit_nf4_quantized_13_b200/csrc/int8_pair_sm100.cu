@@ -94,11 +94,11 @@ struct Pipe {
     __device__ uint32_t drain() const { return bar0 + 8u * (2 * kMaxStages + 4); }
 };
 
-__device__ void role_tma(const Pipe& P, const Params& p, const RowTable& tb, int items, const Maps& maps) {
+__device__ void role_tma(const Pipe& P, const Params& p, const RowTable& tb, const Items& items, const Maps& maps) {
     int s = 0;
     uint32_t ph = 1;
-    for (int it = P.pair; it < items; it += P.num_pairs) {
-        const Item x = item_of(p.q, tb, p.cap, it);
+    for (int it = P.pair; it < items.count; it += P.num_pairs) {
+        const Item x = item_of(p.q, tb, items, p.cap, it);
         const Tile& tl = x.tl;
         const int half = mma_tokens(tl.toks) / 2;
         const int box = box_index(half);
@@ -128,12 +128,12 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int lan
     return ok != 0;
 }
 
-__device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, int items) {
+__device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, const Items& items) {
     const uint64_t a0 = sdesc_kmajor_sw128(P.smem), b0 = sdesc_kmajor_sw128(P.smem + kABytes);
     int s = 0, i = 0;
     uint32_t ph = 0;
-    for (int it = P.pair; it < items; it += P.num_pairs, ++i) {
-        const Item x = item_of(p.q, tb, p.cap, it);
+    for (int it = P.pair; it < items.count; it += P.num_pairs, ++i) {
+        const Item x = item_of(p.q, tb, items, p.cap, it);
         const int b = i & 1;
         const uint32_t idesc = idesc_i8(kRowsPair, mma_tokens(x.tl.toks));
         if (!mbar_wait(P.acc_empty(b), (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u, &g_int8_error)) return;
@@ -186,14 +186,15 @@ __device__ __forceinline__ void store_chunk(const Params& p, const uint32_t (&ac
 }
 
 template <bool kF32>
-__device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb, int items, int warp, int lane) {
+__device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb, const Items& items, int warp, int lane) {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     __shared__ __align__(16) float s_sx[kEpiWarps][kWarpChunks * 32];
     float* sx = s_sx[warp - 2];
     int i = 0;
-    for (int it = P.pair; it < items; it += P.num_pairs, ++i) {
-        const Tile tl = item_of(p.q, tb, p.cap, it).tl;
+    for (int it = P.pair; it < items.count; it += P.num_pairs, ++i) {
+        const Item x = item_of(p.q, tb, items, p.cap, it);
+        const Tile& tl = x.tl;
         const int b = i & 1;
         const int chunks = mma_tokens(tl.toks) / 32;
         const int chan = tl.row0 + static_cast<int>(P.rank) * kRowsCta + quarter * 32 + lane;
@@ -213,10 +214,10 @@ __device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb
             uint32_t acc[32];
             tmem_ld_32x32b_x32(P.tmem + lane_base + static_cast<uint32_t>(b * kTileTok + c * 32), acc);
             tmem_wait_ld();
-            if (p.q.parts == 1)
+            if (x.slot < 0)
                 store_chunk<kF32>(p, acc, sx + (c / 2) * 32, tl, c * 32, chan, sw, lane);
             else
-                slot_store(p.q, it, P.rank, c, quarter * 32 + lane, acc);
+                slot_store(p.q, x.slot, P.rank, c, quarter * 32 + lane, acc);
         }
         tc_fence_before();
         __syncwarp();
@@ -267,7 +268,7 @@ k_int8_gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Para
     cluster_wait();
     tc_fence_after();
     P.tmem = *tmem_slot;
-    const int items = tb.tile0[p.q.E] * p.q.parts;
+    const Items items = items_of(p.q, tb);
     grid_dependency_wait();  // the quantized tokens
     if (warp == 0) {
         if (elect_one()) role_tma(P, p, tb, items, maps);
@@ -362,20 +363,18 @@ int max_pairs() {
 }
 
 template <bool kF32>
-cudaError_t launch_pair(const Maps& maps, const Params& p, int64_t tiles, cudaStream_t st, bool dependent) {
+cudaError_t launch_pair(const Maps& maps, const Params& p, cudaStream_t st, bool dependent) {
     static ContextMemo<int> attr_memo;
     cudaError_t e = ensure_smem_limit(attr_memo, k_int8_gemm_pair<kF32>, kSmemBytes);
     if (e != cudaSuccess) return e;
-    const int most = max_pairs<kF32>();
-    if (most <= 0) return cudaErrorNotSupported;
-    const int64_t items = tiles * p.q.parts;
+    if (max_pairs<kF32>() < 1) return cudaErrorNotSupported;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = pair_config(attr, static_cast<int>(items < most ? items : most), st, dependent);
+    const cudaLaunchConfig_t cfg = pair_config(attr, p.q.pairs, st, dependent);
     e = cudaLaunchKernelEx(&cfg, k_int8_gemm_pair<kF32>, maps, p);
     note_launches(1);
-    if (e != cudaSuccess || p.q.parts == 1) return e;
+    if (e != cudaSuccess || !p.q.slots) return e;
     cudaLaunchAttribute dep[1];
-    const cudaLaunchConfig_t add = add_config(dep, p.q, tiles, st);
+    const cudaLaunchConfig_t add = add_config(dep, p.q, st);
     e = cudaLaunchKernelEx(&add, k_int8_gemm_add<kF32>, p);
     note_launches(1);
     return e;
@@ -389,8 +388,8 @@ int tile_cap(int64_t T, const Int8Weight& w) {
 }
 
 // 500 x 512 x 11008 takes 35 us in whole tiles and 24 in ten parts.
-Schedule schedule(const RowRanges& rr, const Int8Weight& w, int64_t* tiles) {
-    return schedule_of(rr, w.E, w.N, ceil_div(w.K, kBK), tile_cap(rr.T, w), 48, tiles);
+Schedule schedule(const RowRanges& rr, const Int8Weight& w) {
+    return schedule_of(rr, w.E, w.N, ceil_div(w.K, kBK), tile_cap(rr.T, w), 48, sm_pairs());
 }
 
 }  // namespace
@@ -406,20 +405,17 @@ bool int8_pair_supported(int64_t T, const Int8Weight& w) {
 
 // Workspace: the parts' slots.
 size_t int8_pair_workspace(int64_t T, const Int8Weight& w) {
-    int64_t tiles;
-    const Schedule q = schedule(RowRanges{nullptr, T}, w, &tiles);
-    return slots_bytes(q, tiles);
+    return slots_bytes(schedule(RowRanges{nullptr, T}, w), tile_cap(T, w));
 }
 
 cudaError_t launch_int8_fwd_pair(const int8_t* x_codes, const float* x_scale, const Int8Weight& w,
                                  const RowRanges& rr, void* out, int out_dtype, void* ws, cudaStream_t st,
                                  bool dependent) {
-    int64_t tiles;
     Params p{};
     p.xs = x_scale;
     p.ws = w.scale;
-    p.q = schedule(rr, w, &tiles);
-    p.q.slots = static_cast<uint32_t*>(ws);
+    p.q = schedule(rr, w);
+    if (int8_pair_workspace(rr.T, w) > 0) p.q.slots = static_cast<uint32_t*>(ws);
     p.cap = tile_cap(rr.T, w);
     p.stages = ring_stages(p.cap);
     p.stage_bytes = stage_bytes(p.cap);
@@ -429,8 +425,8 @@ cudaError_t launch_int8_fwd_pair(const int8_t* x_codes, const float* x_scale, co
     bool ok = make_map_i8(&maps.w, w.codes, w.K, w.E * w.N, w.ld, kRowsCta);
     for (int i = 0; i < kBoxes; ++i) ok = ok && make_map_i8(&maps.x[i], x_codes, w.K, rr.T, w.ld, box_rows(i));
     if (!ok) return cudaErrorInvalidValue;
-    return out_dtype == 0 ? launch_pair<true>(maps, p, tiles, st, dependent)
-                          : launch_pair<false>(maps, p, tiles, st, dependent);
+    return out_dtype == 0 ? launch_pair<true>(maps, p, st, dependent)
+                          : launch_pair<false>(maps, p, st, dependent);
 }
 
 int int8_device_error(int reset) {

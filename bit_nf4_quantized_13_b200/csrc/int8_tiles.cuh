@@ -100,37 +100,73 @@ __device__ __forceinline__ Tile tile_of(const RowTable& tb, int E, int num_w, in
     return s;
 }
 
-// A schedule: every tile, or (where the tiles leave most pairs of SMs idle: few
-// of them, with a long contraction) each tile's stages cut into `parts` runs
-// for as many pairs.  A part leaves its sums in a workspace slot of its own and
-// a second kernel adds them in order, so no pair waits for another and the
-// result does not depend on the order of arrival.
+// The schedule of a product.  Tiles go round-robin to the pairs of SMs, whole
+// but in the last round: where its tiles leave most pairs idle, each one's
+// stages are cut into `parts` runs for as many pairs.  A part leaves its sums in
+// a workspace slot of its own and a second kernel adds them in order, so no pair
+// waits for another and the result does not depend on the order of arrival.
 struct Schedule {
     RowRanges rr;
     int E;
     int num_w;           // weight-side tiles of one expert
     int kbt;             // stages of a tile
-    int parts;           // parts of a tile
-    uint32_t* slots;     // parts > 1: a slot for each part
+    int min_saved;       // stages that parts must take off a pair's work
+    int pairs;           // of the launch
+    uint32_t* slots;     // a slot for each part (at most `pairs`); nullptr: whole tiles only
     int64_t slot_words;  // 256 rows of the widest tile's tokens
 };
 
-// One part of a tile.
+// The last round of `tiles` tiles: its first tile and their parts, as many as
+// give every pair one, of at least kMinStages stages.  Adding them costs about 5
+// us and 0.4 us a part, so they end at kMaxParts.
+constexpr int kMinStages = 8, kMaxParts = 16;
+struct Tail {
+    int first, parts;
+};
+__host__ __device__ inline Tail tail_of(const Schedule& q, int tiles, int pairs) {
+    Tail t;
+    t.first = tiles / pairs * pairs;
+    const int left = tiles - t.first;
+    int parts = left > 0 ? pairs / left : 1;
+    if (parts > q.kbt / kMinStages) parts = q.kbt / kMinStages;
+    if (parts > kMaxParts) parts = kMaxParts;
+    t.parts = parts > 1 && q.kbt - q.kbt / parts >= q.min_saved ? parts : 1;
+    return t;
+}
+
+// What the pairs work on: the items of one launch, in shared memory.
+struct Items {
+    int count;
+    Tail tail;
+};
+__device__ __forceinline__ Items items_of(const Schedule& q, const RowTable& tb) {
+    Items x;
+    const int tiles = tb.tile0[q.E];
+    x.tail = q.slots ? tail_of(q, tiles, q.pairs) : Tail{tiles, 1};
+    x.count = x.tail.first + (tiles - x.tail.first) * x.tail.parts;
+    return x;
+}
+
+// One item: a tile, or a part of one.
 struct Item {
     Tile tl;
     int kb0, stages;
+    int slot;  // -1: the whole tile
 };
 
-__device__ __forceinline__ Item item_of(const Schedule& q, const RowTable& tb, int cap, int it) {
+__device__ __forceinline__ Item item_of(const Schedule& q, const RowTable& tb, const Items& items, int cap, int it) {
     Item x;
     int tile = it;
     x.kb0 = 0;
     x.stages = q.kbt;
-    if (q.parts > 1) {
-        tile = it / q.parts;
-        const int part = it - tile * q.parts;
-        x.kb0 = part * q.kbt / q.parts;
-        x.stages = (part + 1) * q.kbt / q.parts - x.kb0;
+    x.slot = -1;
+    const int parts = items.tail.parts;
+    if (parts > 1 && it >= items.tail.first) {
+        x.slot = it - items.tail.first;
+        const int t = x.slot / parts, part = x.slot - t * parts;
+        tile = items.tail.first + t;
+        x.kb0 = part * q.kbt / parts;
+        x.stages = (part + 1) * q.kbt / parts - x.kb0;
     }
     x.tl = tile_of(tb, q.E, q.num_w, cap, tile);
     return x;
@@ -150,9 +186,9 @@ __device__ __forceinline__ void slot_store(const Schedule& q, int slot, uint32_t
         *slot_at(q, slot, rank, chunk, g, row) = make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
 }
 
-// The adding kernel's block (tile, chunk of 32 tokens, CTA) of kAddThreads, a
-// row each: the tile and the row's sums over the parts (kInt: integers, else
-// fp32); false where the tile has no such chunk.
+// The adding kernel's block (tile of the last round, chunk of 32 tokens, CTA)
+// of kAddThreads, a row each: the tile and the row's sums over the parts (kInt:
+// integers, else fp32); false where there is no such tile or chunk.
 constexpr int kAddThreads = kTileRows / 2;
 template <bool kInt>
 __device__ __forceinline__ bool add_parts(const Schedule& q, int cap, Tile* tl, uint32_t (&v)[32]) {
@@ -160,19 +196,20 @@ __device__ __forceinline__ bool add_parts(const Schedule& q, int cap, Tile* tl, 
     const RowTable tb = row_table(s_table);
     if (threadIdx.x < 32) build_table(q.rr, q.E, q.num_w, cap, tb, static_cast<int>(threadIdx.x));
     __syncthreads();
-    const int tile = static_cast<int>(blockIdx.x), chunk = static_cast<int>(blockIdx.y);
+    const int tiles = tb.tile0[q.E], t = static_cast<int>(blockIdx.x), chunk = static_cast<int>(blockIdx.y);
+    const Tail tail = tail_of(q, tiles, q.pairs);
     sm100::grid_dependency_wait();  // the parts' sums
-    if (tile >= tb.tile0[q.E]) return false;
-    *tl = tile_of(tb, q.E, q.num_w, cap, tile);
+    if (tail.parts == 1 || tail.first + t >= tiles) return false;
+    *tl = tile_of(tb, q.E, q.num_w, cap, tail.first + t);
     if (chunk * 32 >= tl->toks) return false;
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = 0u;  // the bits of 0.0f too
 #pragma unroll 2
-    for (int j = 0; j < q.parts; ++j) {
+    for (int j = 0; j < tail.parts; ++j) {
         uint4 x[8];
 #pragma unroll
         for (int g = 0; g < 8; ++g)
-            x[g] = __ldcg(slot_at(q, tile * q.parts + j, blockIdx.z, chunk, g, static_cast<int>(threadIdx.x)));
+            x[g] = __ldcg(slot_at(q, t * tail.parts + j, blockIdx.z, chunk, g, static_cast<int>(threadIdx.x)));
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
             const uint32_t y[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
@@ -186,39 +223,43 @@ __device__ __forceinline__ bool add_parts(const Schedule& q, int cap, Tile* tl, 
     return true;
 }
 
-// The most tiles of a problem, and the parts each is cut into: as many as give
-// every pair of SMs one, of at least kMinStages stages, if that takes
-// `min_saved` stages off a pair's work.  Adding them costs about 5 us and 0.4
-// us a part, so they end at kMaxParts.
-constexpr int kMinStages = 8, kMaxParts = 16;
+// The schedule for `most` pairs at most, without its slots.
 inline Schedule schedule_of(const RowRanges& rr, int E, int64_t w_rows, int64_t kbt, int cap, int min_saved,
-                            int64_t* tiles) {
+                            int64_t most) {
     Schedule q{};
     q.rr = rr;
     q.E = E;
     q.num_w = static_cast<int>(ceil_div(w_rows, kTileRows));
     q.kbt = static_cast<int>(kbt);
+    q.min_saved = min_saved;
     q.slot_words = static_cast<int64_t>(kTileRows) * (rr.T < cap ? round_up(rr.T, 32) : cap);
-    *tiles = E == 1 ? static_cast<int64_t>(token_tiles(static_cast<int>(rr.T), cap)) * q.num_w
-                    : int8_tiles(rr.T, E, w_rows, cap);
-    const int64_t pairs = num_sms() / 2 > 0 ? num_sms() / 2 : 1;
-    int64_t parts = pairs / (*tiles > 0 ? *tiles : 1);
-    if (parts > kbt / kMinStages) parts = kbt / kMinStages;
-    if (parts > kMaxParts) parts = kMaxParts;
-    q.parts = parts > 1 && kbt - kbt / parts >= min_saved ? static_cast<int>(parts) : 1;
+    // no more pairs than there can be items
+    int64_t parts = kbt / kMinStages < kMaxParts ? kbt / kMinStages : kMaxParts;
+    if (parts < 1) parts = 1;
+    const int64_t tiles = E == 1 ? static_cast<int64_t>(token_tiles(static_cast<int>(rr.T), cap)) * q.num_w
+                                 : int8_tiles(rr.T, E, w_rows, cap);
+    q.pairs = static_cast<int>(tiles * parts < most ? tiles * parts : most);
     return q;
 }
-inline size_t slots_bytes(const Schedule& q, int64_t tiles) {
-    return q.parts == 1 ? 0 : static_cast<size_t>(tiles * q.parts * q.slot_words) * 4;
+
+// Bytes of its slots: none where no tile will be cut, which for a dense product
+// (every row, one weight) is known here; for experts only the device knows.
+inline size_t slots_bytes(const Schedule& q, int cap) {
+    const int parts = q.kbt / kMinStages < kMaxParts ? q.kbt / kMinStages : kMaxParts;
+    if (parts < 2 || q.kbt - q.kbt / parts < q.min_saved) return 0;
+    if (q.E == 1 && tail_of(q, token_tiles(static_cast<int>(q.rr.T), cap) * q.num_w, q.pairs).parts == 1) return 0;
+    return static_cast<size_t>(q.pairs * q.slot_words) * 4;
 }
 
-// The adding kernel's launch, dependent on the product's.
-inline cudaLaunchConfig_t add_config(cudaLaunchAttribute (&attr)[1], const Schedule& q, int64_t tiles,
-                                     cudaStream_t st) {
+inline int sm_pairs() { return num_sms() / 2 > 0 ? num_sms() / 2 : 1; }
+
+// The adding kernel's launch, dependent on the product's: a tile of the last
+// round is cut only if there are two pairs for it.
+inline cudaLaunchConfig_t add_config(cudaLaunchAttribute (&attr)[1], const Schedule& q, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(q.slot_words / kTileRows / 32), 2);
+    cfg.gridDim = dim3(static_cast<unsigned>(q.pairs / 2), static_cast<unsigned>(q.slot_words / kTileRows / 32), 2);
     cfg.blockDim = dim3(kAddThreads);
     cfg.stream = st;
     cfg.attrs = attr;

@@ -95,13 +95,6 @@ size_t int8_dx_workspace(int64_t T, const Int8Weight& w);
 cudaError_t launch_int8_dx(const uint16_t* dY, const Int8Weight& w, const RowRanges& rr, uint16_t* dX, void* ws,
                            cudaStream_t stream);
 int int8_dx_device_error(int reset);
-// int8_dx_narrow_sm100.cu -- the same for tiles of up to 256 tokens; dY's rows
-// are ldy (a multiple of 8) elements apart; ws: int8_dx_narrow_workspace bytes
-int int8_dx_narrow_parts(int64_t T, const Int8Weight& w);
-size_t int8_dx_narrow_workspace(int64_t T, const Int8Weight& w);
-cudaError_t launch_int8_dx_narrow(const uint16_t* dY, int64_t ldy, const Int8Weight& w, const RowRanges& rr,
-                                  uint16_t* dX, void* ws, cudaStream_t stream);
-int int8_dx_narrow_device_error(int reset);
 
 // The frozen NF4 weight W (N x K row-major) as the GEMM kernels see it.
 struct Nf4Weight {

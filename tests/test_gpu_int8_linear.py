@@ -220,7 +220,7 @@ EXPERT_CASES = [
     ([0] * 60 + [700] + [0] * 3, 0, 0, 72, 640),
     ([7] * 128, 0, 0, 96, 160),
     ([0, 1] * 500, 5, 5, 17, 33),
-    ([3900, 100, 0, 150], 1, 3, 72, 300),   # 1024 rows an expert and more: wide gradient tiles, and small ones among them
+    ([3900, 100, 0, 150], 1, 3, 72, 300),   # many full tiles, small ones among them
     ([1500, 2600, 1025], 0, 0, 65, 513),
     ([5, 0, 30], 2, 1, 5000, 130),          # few tiles, a long contraction of the gradient
     ([300, 20], 0, 4, 4097, 64),
