@@ -124,7 +124,7 @@ struct Ring {
 __device__ void role_tokens(const Pipe& P, const Params& p, const RowTable& tb, const Items& items, const Maps& maps) {
     Ring<kStages> ring{0, 1};
     for (int it = P.pair; it < items.count; it += P.num_pairs) {
-        const Item x = item_of(p.q, tb, items, kTileTok, it);
+        const Item x = item_of(p.q, tb, items, it);
         const Tile& tl = x.tl;
         const int half = mma_tokens(tl.toks) / 2, box = box_index(half);
         const int row = tl.tok0 + static_cast<int>(P.rank) * half;
@@ -140,7 +140,7 @@ __device__ void role_tokens(const Pipe& P, const Params& p, const RowTable& tb, 
 __device__ void role_codes(const Pipe& P, const Params& p, const RowTable& tb, const Items& items, const Maps& maps) {
     Ring<kRaw> ring{0, 1};
     for (int it = P.pair; it < items.count; it += P.num_pairs) {
-        const Item x = item_of(p.q, tb, items, kTileTok, it);
+        const Item x = item_of(p.q, tb, items, it);
         const int col = x.tl.row0 + static_cast<int>(P.rank) * kRowsCta, n0 = x.tl.expert * p.N;
         for (int kb = x.kb0; kb < x.kb0 + x.stages; ++kb, ring.step(1)) {
             if (!mbar_wait(P.raw_empty(ring.slot), ring.turn, &g_int8_dx_error)) return;
@@ -161,7 +161,7 @@ __device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, con
     Ring<kStages> ring{0, 0};
     int i = 0;
     for (int it = P.pair; it < items.count; it += P.num_pairs, ++i) {
-        const Item x = item_of(p.q, tb, items, kTileTok, it);
+        const Item x = item_of(p.q, tb, items, it);
         const uint32_t idesc = idesc_bf16(kTileRows, mma_tokens(x.tl.toks), 1, 0);
         const int b = i & 1;
         if (!mbar_wait(P.acc_empty(b), (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u, &g_int8_dx_error)) return;
@@ -205,7 +205,7 @@ __device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb,
     uint32_t turn = 1;
     int kb = part;  // this part's next stage, counted from the item's first
     for (int it = P.pair; it < items.count; it += P.num_pairs) {
-        const Item x = item_of(p.q, tb, items, kTileTok, it);
+        const Item x = item_of(p.q, tb, items, it);
         const float* scale = p.scale + static_cast<int64_t>(x.tl.expert) * p.N;
         for (; kb < x.stages; kb += kParts) {
             // rows past N hold other codes or zeros: scale 0 makes them 0
@@ -260,7 +260,7 @@ __device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     int i = 0;
     for (int it = P.pair; it < items.count; it += P.num_pairs, ++i) {
-        const Item x = item_of(p.q, tb, items, kTileTok, it);
+        const Item x = item_of(p.q, tb, items, it);
         const int b = i & 1, row = quarter * 32 + lane;
         if (!warp_wait(P.acc_full(b), static_cast<uint32_t>(i >> 1) & 1u)) return;
         tc_fence_after();
@@ -320,7 +320,7 @@ k_int8_dx_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params
         tma_prefetch_desc(&maps.w);
         for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.y[i]);
     }
-    if (warp == 2) build_table(p.q.rr, p.q.E, p.q.num_w, kTileTok, tb, lane);
+    if (warp == 2) build_table(p.q, tb, lane);
     tc_fence_before();
     __syncthreads();
     cluster_arrive();  // both CTAs' barriers are initialised before any remote arrive
@@ -361,7 +361,7 @@ k_int8_dx_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params
 __global__ void __launch_bounds__(kAddThreads) k_int8_dx_add(const __grid_constant__ Params p) {
     Tile tl;
     uint32_t sums[32];
-    if (add_parts<false>(p.q, kTileTok, &tl, sums))
+    if (add_parts<false>(p.q, &tl, sums))
         store_sums(p, sums, tl, static_cast<int>(blockIdx.y) * 32,
                    tl.row0 + static_cast<int>(blockIdx.z) * kRowsCta + static_cast<int>(threadIdx.x), threadIdx.x & 31);
 }
@@ -439,7 +439,7 @@ size_t padded_bytes(int64_t T, const Int8Weight& w) {
     return w.N % 8 == 0 ? 0 : static_cast<size_t>(round_up(T * round_up(w.N, 8) * 2, 256));
 }
 size_t parts_bytes(int64_t T, const Int8Weight& w) {
-    return slots_bytes(schedule(RowRanges{nullptr, T}, w), kTileTok);
+    return slots_bytes(schedule(RowRanges{nullptr, T}, w));
 }
 
 }  // namespace

@@ -22,8 +22,6 @@
 // Two accumulators of 256 columns alternate, so a tile's epilogue runs under
 // the next tile's MMAs.
 //
-// Tiles go round-robin to the pairs.
-//
 // Every mbarrier wait is bounded; a timeout records QLORA_ERR_TIMEOUT in a
 // sticky device word and ends the role.
 #include <cudaTypedefs.h>
@@ -65,16 +63,17 @@ struct Params {
     const float* ws;   // E x N channel scales
     Schedule q;        // weight tiles: ceil(N / 256); stages: ceil(K / 128)
     int N;
-    int cap;           // most tokens of a tile
     int stages;        // of the ring
     int stage_bytes;   // the weight's 16 KiB, then half of the tokens
     void* out;
 };
 
-// The ring for tiles of up to `cap` tokens (64, 128 or 256): the smaller the
-// tokens' part of a stage, the more stages are in flight, which is what the
-// weight stream of small tiles needs.
-__host__ __device__ constexpr int stage_bytes(int cap) { return kABytes + cap / 2 * kBK; }
+// The ring for tiles of up to `cap` tokens: the smaller the tokens' part of a
+// stage (boxes for 64, 128 or 256), the more stages are in flight, which is
+// what the weight stream of small tiles needs.
+__host__ __device__ constexpr int stage_bytes(int cap) {
+    return kABytes + (cap > 128 ? kTileTok : cap > 64 ? 128 : 64) / 2 * kBK;
+}
 __host__ __device__ constexpr int ring_stages(int cap) { return kRingBytes / stage_bytes(cap); }
 static_assert(ring_stages(64) == kMaxStages && ring_stages(128) == 8 && ring_stages(kTileTok) == 6, "rings");
 static_assert(8 * (2 * kMaxStages + 5) + 4 <= kTableOff - kBarOff, "barriers and the TMEM address");
@@ -98,7 +97,7 @@ __device__ void role_tma(const Pipe& P, const Params& p, const RowTable& tb, con
     int s = 0;
     uint32_t ph = 1;
     for (int it = P.pair; it < items.count; it += P.num_pairs) {
-        const Item x = item_of(p.q, tb, items, p.cap, it);
+        const Item x = item_of(p.q, tb, items, it);
         const Tile& tl = x.tl;
         const int half = mma_tokens(tl.toks) / 2;
         const int box = box_index(half);
@@ -133,7 +132,7 @@ __device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, con
     int s = 0, i = 0;
     uint32_t ph = 0;
     for (int it = P.pair; it < items.count; it += P.num_pairs, ++i) {
-        const Item x = item_of(p.q, tb, items, p.cap, it);
+        const Item x = item_of(p.q, tb, items, it);
         const int b = i & 1;
         const uint32_t idesc = idesc_i8(kRowsPair, mma_tokens(x.tl.toks));
         if (!mbar_wait(P.acc_empty(b), (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u, &g_int8_error)) return;
@@ -193,7 +192,7 @@ __device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb
     float* sx = s_sx[warp - 2];
     int i = 0;
     for (int it = P.pair; it < items.count; it += P.num_pairs, ++i) {
-        const Item x = item_of(p.q, tb, items, p.cap, it);
+        const Item x = item_of(p.q, tb, items, it);
         const Tile& tl = x.tl;
         const int b = i & 1;
         const int chunks = mma_tokens(tl.toks) / 32;
@@ -261,7 +260,7 @@ k_int8_gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Para
         tma_prefetch_desc(&maps.w);
         for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.x[i]);
     }
-    if (warp == 2) build_table(p.q.rr, p.q.E, p.q.num_w, p.cap, tb, lane);
+    if (warp == 2) build_table(p.q, tb, lane);
     tc_fence_before();
     __syncthreads();
     cluster_arrive();  // both CTAs' barriers are initialised before any remote arrive
@@ -302,7 +301,7 @@ __global__ void __launch_bounds__(kAddThreads) k_int8_gemm_add(const __grid_cons
     const int tok = static_cast<int>(blockIdx.y) * 32, lane = threadIdx.x & 31;
     Tile tl;
     uint32_t sums[32];
-    if (!add_parts<true>(p.q, p.cap, &tl, sums)) return;
+    if (!add_parts<true>(p.q, &tl, sums)) return;
     if (threadIdx.x < 32) s_sx[lane] = tok + lane < tl.toks ? p.xs[tl.tok0 + tok + lane] : 0.0f;
     __syncthreads();
     const int chan = tl.row0 + static_cast<int>(blockIdx.z) * kRowsCta + static_cast<int>(threadIdx.x);
@@ -380,17 +379,46 @@ cudaError_t launch_pair(const Maps& maps, const Params& p, cudaStream_t st, bool
     return e;
 }
 
-// The most tokens of a tile.  Dense: the batch decides.  Experts: their average
-// rows do (an expert with more takes its weight through the L2 once a tile).
-int tile_cap(int64_t T, const Int8Weight& w) {
-    const int64_t m = ceil_div(T, T < w.E ? T : w.E);
-    return m <= 64 ? 64 : m <= 128 ? 128 : kTileTok;
+Schedule schedule_with(const RowRanges& rr, const Int8Weight& w, int cap) {
+    // 500 x 512 x 11008 takes 35 us in whole tiles and 24 in ten parts
+    return schedule_of(rr, w.E, w.N, ceil_div(w.K, kBK), cap, 48, sm_pairs());
 }
 
-// 500 x 512 x 11008 takes 35 us in whole tiles and 24 in ten parts.
-Schedule schedule(const RowRanges& rr, const Int8Weight& w) {
-    return schedule_of(rr, w.E, w.N, ceil_div(w.K, kBK), tile_cap(rr.T, w), 48, sm_pairs());
+// Cycles of the pairs' rounds over T rows of one weight.  Measured on 72 tiles
+// (one round): a stage of m tokens takes 270 cycles for m = 64, 317 for 128, 470
+// for 192, 590 for 256; a tile begins and ends in about 1500; adding parts takes
+// 5 us and 0.4 us a part.
+int64_t cycles(const Schedule& q) {
+    const int T = static_cast<int>(q.rr.T), tiles = token_tiles(T, q.cap) * q.num_w;
+    const Tail tail = tail_of(q, tiles, q.pairs);
+    const int64_t stage = 180 + token_width(T, q.cap) * 8 / 5;
+    int64_t c = tail.first / q.pairs * (q.kbt * stage + 1500);
+    if (tail.first < tiles) c += (q.kbt + tail.parts - 1) / tail.parts * stage + 1500;
+    return tail.parts > 1 ? c + 9500 + 760 * tail.parts : c;
 }
+
+// The most tokens of a tile.  Dense: the width whose rounds take the fewest
+// cycles (with tiles of 256 only, 512 x 4096 x 11008 takes 39 us in place of 29,
+// 777 x 5120 x 5120 33 in place of 27; 39 of 40 shapes of 200 to 3000 tokens are
+// within 10% of the best width).  Experts: their average rows decide (an expert
+// with more takes its weight through the L2 once a tile).
+int tile_cap(int64_t T, const Int8Weight& w) {
+    const int64_t m = ceil_div(T, T < w.E ? T : w.E);
+    if (m <= 64) return 64;
+    if (w.E > 1) return m <= 128 ? 128 : kTileTok;
+    int best = 0;
+    int64_t least = 0;
+    for (int cap = kTileTok; cap >= 64; cap -= 32) {
+        const int64_t c = cycles(schedule_with(RowRanges{nullptr, T}, w, cap));
+        if (best == 0 || c < least) {
+            best = cap;
+            least = c;
+        }
+    }
+    return token_width(static_cast<int>(T), best);
+}
+
+Schedule schedule(const RowRanges& rr, const Int8Weight& w) { return schedule_with(rr, w, tile_cap(rr.T, w)); }
 
 }  // namespace
 
@@ -405,7 +433,7 @@ bool int8_pair_supported(int64_t T, const Int8Weight& w) {
 
 // Workspace: the parts' slots.
 size_t int8_pair_workspace(int64_t T, const Int8Weight& w) {
-    return slots_bytes(schedule(RowRanges{nullptr, T}, w), tile_cap(T, w));
+    return slots_bytes(schedule(RowRanges{nullptr, T}, w));
 }
 
 cudaError_t launch_int8_fwd_pair(const int8_t* x_codes, const float* x_scale, const Int8Weight& w,
@@ -416,9 +444,8 @@ cudaError_t launch_int8_fwd_pair(const int8_t* x_codes, const float* x_scale, co
     p.ws = w.scale;
     p.q = schedule(rr, w);
     if (int8_pair_workspace(rr.T, w) > 0) p.q.slots = static_cast<uint32_t*>(ws);
-    p.cap = tile_cap(rr.T, w);
-    p.stages = ring_stages(p.cap);
-    p.stage_bytes = stage_bytes(p.cap);
+    p.stages = ring_stages(p.q.cap);
+    p.stage_bytes = stage_bytes(p.q.cap);
     p.N = static_cast<int>(w.N);
     p.out = out;
     Maps maps;

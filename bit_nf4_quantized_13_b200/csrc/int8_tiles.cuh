@@ -31,11 +31,28 @@ __host__ __device__ inline int token_width(int m, int cap) {
     return t > 0 ? ((m + t - 1) / t + 31) & ~31 : 0;
 }
 
+// The schedule of a product.  Tiles go round-robin to the pairs of SMs, whole
+// but in the last round: where its tiles leave most pairs idle, each one's
+// stages are cut into `parts` runs for as many pairs.  A part leaves its sums in
+// a workspace slot of its own and a second kernel adds them in order, so no pair
+// waits for another and the result does not depend on the order of arrival.
+struct Schedule {
+    RowRanges rr;
+    int E;
+    int num_w;           // weight-side tiles of one expert
+    int cap;             // most tokens of a tile
+    int kbt;             // stages of a tile
+    int min_saved;       // stages that parts must take off a pair's work
+    int pairs;           // of the launch
+    uint32_t* slots;     // a slot for each part (at most `pairs`); nullptr: whole tiles only
+    int64_t slot_words;  // 256 rows of the widest tile's tokens
+};
+
 // Filled by one warp.  An offset counts as no less than the one before it and
 // at most T, so the ranges are disjoint and inside the rows whatever it holds.
-// num_w: weight-side tiles of one expert.
-__device__ __forceinline__ void build_table(const RowRanges& rr, int E, int num_w, int cap, const RowTable& tb,
-                                            int lane) {
+__device__ __forceinline__ void build_table(const Schedule& q, const RowTable& tb, int lane) {
+    const RowRanges& rr = q.rr;
+    const int E = q.E;
     const int T = static_cast<int>(rr.T);
     int top = 0, tiles = 0;  // the last offset and the tiles so far
     if (rr.offsets) top = min(max(rr.offsets[0], 0), T);
@@ -52,7 +69,7 @@ __device__ __forceinline__ void build_table(const RowRanges& rr, int E, int num_
         for (int o = 1; o < 32; o <<= 1) hi = max(hi, __shfl_up_sync(0xffffffffu, hi, o));  // lanes < o: their own
         int lo = __shfl_up_sync(0xffffffffu, hi, 1);
         if (lane == 0) lo = top;
-        int n = e < E ? token_tiles(hi - lo, cap) * num_w : 0;
+        int n = e < E ? token_tiles(hi - lo, q.cap) * q.num_w : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int up = __shfl_up_sync(0xffffffffu, n, o);
@@ -75,9 +92,9 @@ struct Tile {
 // Tile `unit`: experts in order; inside an expert bands of kBand weight tiles
 // with the token tiles slowest in a band, so that the pairs at work at the
 // same time cover a compact block of tokens and weights (kept in L2).
-__device__ __forceinline__ Tile tile_of(const RowTable& tb, int E, int num_w, int cap, int unit) {
+__device__ __forceinline__ Tile tile_of(const Schedule& q, const RowTable& tb, int unit) {
     constexpr int kBand = 8;
-    int e = 0, above = E;  // tile0[e] <= unit < tile0[above]
+    int e = 0, above = q.E;  // tile0[e] <= unit < tile0[above]
     while (above - e > 1) {
         const int c = (e + above) >> 1;
         if (tb.tile0[c] <= unit)
@@ -87,10 +104,10 @@ __device__ __forceinline__ Tile tile_of(const RowTable& tb, int E, int num_w, in
     }
     const int lo = tb.off[e], hi = tb.off[e + 1];
     const int u = unit - tb.tile0[e];
-    const int num_t = token_tiles(hi - lo, cap), width = token_width(hi - lo, cap);
+    const int num_t = token_tiles(hi - lo, q.cap), width = token_width(hi - lo, q.cap);
     const int band_tiles = kBand * num_t;
     const int band = u / band_tiles, in = u % band_tiles;
-    const int rows_in_band = min(kBand, num_w - band * kBand);
+    const int rows_in_band = min(kBand, q.num_w - band * kBand);
     const int t = in / rows_in_band;
     Tile s;
     s.expert = e;
@@ -99,22 +116,6 @@ __device__ __forceinline__ Tile tile_of(const RowTable& tb, int E, int num_w, in
     s.toks = min(width, hi - s.tok0);
     return s;
 }
-
-// The schedule of a product.  Tiles go round-robin to the pairs of SMs, whole
-// but in the last round: where its tiles leave most pairs idle, each one's
-// stages are cut into `parts` runs for as many pairs.  A part leaves its sums in
-// a workspace slot of its own and a second kernel adds them in order, so no pair
-// waits for another and the result does not depend on the order of arrival.
-struct Schedule {
-    RowRanges rr;
-    int E;
-    int num_w;           // weight-side tiles of one expert
-    int kbt;             // stages of a tile
-    int min_saved;       // stages that parts must take off a pair's work
-    int pairs;           // of the launch
-    uint32_t* slots;     // a slot for each part (at most `pairs`); nullptr: whole tiles only
-    int64_t slot_words;  // 256 rows of the widest tile's tokens
-};
 
 // The last round of `tiles` tiles: its first tile and their parts, as many as
 // give every pair one, of at least kMinStages stages.  Adding them costs about 5
@@ -154,7 +155,7 @@ struct Item {
     int slot;  // -1: the whole tile
 };
 
-__device__ __forceinline__ Item item_of(const Schedule& q, const RowTable& tb, const Items& items, int cap, int it) {
+__device__ __forceinline__ Item item_of(const Schedule& q, const RowTable& tb, const Items& items, int it) {
     Item x;
     int tile = it;
     x.kb0 = 0;
@@ -168,7 +169,7 @@ __device__ __forceinline__ Item item_of(const Schedule& q, const RowTable& tb, c
         x.kb0 = part * q.kbt / parts;
         x.stages = (part + 1) * q.kbt / parts - x.kb0;
     }
-    x.tl = tile_of(tb, q.E, q.num_w, cap, tile);
+    x.tl = tile_of(q, tb, tile);
     return x;
 }
 
@@ -191,16 +192,16 @@ __device__ __forceinline__ void slot_store(const Schedule& q, int slot, uint32_t
 // integers, else fp32); false where there is no such tile or chunk.
 constexpr int kAddThreads = kTileRows / 2;
 template <bool kInt>
-__device__ __forceinline__ bool add_parts(const Schedule& q, int cap, Tile* tl, uint32_t (&v)[32]) {
+__device__ __forceinline__ bool add_parts(const Schedule& q, Tile* tl, uint32_t (&v)[32]) {
     __shared__ int s_table[kRowTableBytes / 4];
     const RowTable tb = row_table(s_table);
-    if (threadIdx.x < 32) build_table(q.rr, q.E, q.num_w, cap, tb, static_cast<int>(threadIdx.x));
+    if (threadIdx.x < 32) build_table(q, tb, static_cast<int>(threadIdx.x));
     __syncthreads();
     const int tiles = tb.tile0[q.E], t = static_cast<int>(blockIdx.x), chunk = static_cast<int>(blockIdx.y);
     const Tail tail = tail_of(q, tiles, q.pairs);
     sm100::grid_dependency_wait();  // the parts' sums
     if (tail.parts == 1 || tail.first + t >= tiles) return false;
-    *tl = tile_of(tb, q.E, q.num_w, cap, tail.first + t);
+    *tl = tile_of(q, tb, tail.first + t);
     if (chunk * 32 >= tl->toks) return false;
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = 0u;  // the bits of 0.0f too
@@ -230,6 +231,7 @@ inline Schedule schedule_of(const RowRanges& rr, int E, int64_t w_rows, int64_t 
     q.rr = rr;
     q.E = E;
     q.num_w = static_cast<int>(ceil_div(w_rows, kTileRows));
+    q.cap = cap;
     q.kbt = static_cast<int>(kbt);
     q.min_saved = min_saved;
     q.slot_words = static_cast<int64_t>(kTileRows) * (rr.T < cap ? round_up(rr.T, 32) : cap);
@@ -244,10 +246,10 @@ inline Schedule schedule_of(const RowRanges& rr, int E, int64_t w_rows, int64_t 
 
 // Bytes of its slots: none where no tile will be cut, which for a dense product
 // (every row, one weight) is known here; for experts only the device knows.
-inline size_t slots_bytes(const Schedule& q, int cap) {
+inline size_t slots_bytes(const Schedule& q) {
     const int parts = q.kbt / kMinStages < kMaxParts ? q.kbt / kMinStages : kMaxParts;
-    if (parts < 2 || q.kbt - q.kbt / parts < q.min_saved) return 0;
-    if (q.E == 1 && tail_of(q, token_tiles(static_cast<int>(q.rr.T), cap) * q.num_w, q.pairs).parts == 1) return 0;
+    if (parts < 2 || q.pairs < 2 || q.kbt - q.kbt / parts < q.min_saved) return 0;
+    if (q.E == 1 && tail_of(q, token_tiles(static_cast<int>(q.rr.T), q.cap) * q.num_w, q.pairs).parts == 1) return 0;
     return static_cast<size_t>(q.pairs * q.slot_words) * 4;
 }
 

@@ -381,3 +381,97 @@ def test_an_expert_block_forward_and_back():
             ref.check_backward(got[s], d[s], compute_weight(w, e), f"expert {e}")
     for t in (G, U, Y, dA, *dX):
         assert not t[o[-1]:].any()
+
+
+@pytest.mark.parametrize("M,N,K", [(200, 4100, 1024), (300, 5120, 640), (400, 2560, 6200), (512, 4608, 300),
+                                   (777, 5000, 512), (1500, 5120, 256), (512, 2049, 7000), (200, 5000, 9000)])
+def test_linear_fwd_between_the_tile_widths(M, N, K):
+    """Batches of a few tiles, whose width follows the number of SM pairs."""
+    X, w = tokens(M + N, M, K), weight(K, N, K)
+    ref.check_forward(q.qlora_int8_linear_fwd(X, w), fwd_ref(X, w), "Y")
+    assert q.qlora_device_error() == 0
+
+
+def test_two_streams_at_once():
+    """Independent calls on two streams, each with its own buffers."""
+    T, E, N, K = 700, 4, 1100, 2048
+    w = weight(3, E, N, K)
+    X, dY = tokens(1, T, K), tokens(2, T, N, 0.01)
+    off = offsets_of([100, 0, 350, 200], 7)
+    full = lambda n: torch.full((T, n), 7.0, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    Y0, dX0 = q.qlora_int8_expert_fwd(X, w, off, Y=full(N)), q.qlora_int8_expert_bwd(dY, w, off, dX=full(K))
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    bufs = [[(full(N), full(K)) for _ in range(10)] for _ in streams]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for i in range(10):
+        for s, b in zip(streams, bufs):
+            outs.append((q.qlora_int8_expert_fwd(X, w, off, Y=b[i][0], stream=s),
+                         q.qlora_int8_expert_bwd(dY, w, off, dX=b[i][1], stream=s)))
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    for Y, dX in outs:
+        assert torch.equal(Y, Y0) and torch.equal(dX, dX0)
+    assert q.qlora_device_error() == 0
+
+
+def test_two_graphs_on_one_workspace():
+    """Graphs replayed in turn on one stream may share a workspace."""
+    M, N, K = 500, 512, 11008
+    w, shapes = weight(4, N, K), ((500, 1), (300, 2))
+    need = max(max(q.qlora_int8_linear_fwd_workspace_size(m, N, K), q.qlora_int8_linear_bwd_workspace_size(m, N, K))
+               for m, _ in shapes)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    runs = []
+    for m, seed in shapes:
+        X, dY = tokens(seed, m, K), tokens(seed + 5, m, N, 0.01)
+        want = q.qlora_int8_linear_fwd(X, w), q.qlora_int8_linear_bwd(dY, w)
+        got = torch.empty_like(want[0]), torch.empty_like(want[1])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            q.qlora_int8_linear_fwd(X, w, Y=got[0], ws=ws)
+            q.qlora_int8_linear_bwd(dY, w, dX=got[1], ws=ws)
+        runs.append((graph, X, dY, want, got))
+    ws.fill_(255)
+    for _ in range(3):
+        for graph, _, _, _, got in runs:
+            for t in got:
+                t.fill_(float("nan"))
+            graph.replay()
+        for _, _, _, want, got in runs:
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def check_ends(M, a, b, check):
+    for s in (slice(0, 3), slice(M - 70, M)):
+        check(a[s], b[s])
+
+
+def test_offsets_past_32_bits():
+    """Tokens, outputs and gradients of more than 2^31 elements, and weights of
+    more than 2^31 codes: the last rows are as right as the first."""
+    M, big, few = (1 << 20) + 77, 2064, 24
+    X, w = tokens(1, M, few), weight(2, big, few)
+    Y = q.qlora_int8_linear_fwd(X, w)
+    check_ends(M, X, Y, lambda x, y: ref.check_forward(y, fwd_ref(x, w), "wide output"))
+    del Y
+    w = weight(3, few, big)
+    dX = q.qlora_int8_linear_bwd(X, w)
+    check_ends(M, X, dX, lambda d, x: ref.check_backward(x, d, compute_weight(w), "gradient"))
+    Y = q.qlora_int8_linear_fwd(dX, w)
+    check_ends(M, dX, Y, lambda x, y: ref.check_forward(y, fwd_ref(x, w), "long input"))
+    del dX, Y, X
+    E, N, K = 66, 8000, 4112
+    w = q.alloc_int8_rows((E, N, K), "cuda")
+    for e in range(E):
+        q.qlora_int8_quantize_rows(torch.randn((N, K), generator=gen(e), device="cuda") * 0.02,
+                                   out=q.Int8Rows(w.codes[e], w.scale[e], (N, K)))
+    for counts in ([3] + [0] * 64 + [4], [30] + [0] * 64 + [100]):
+        off, T = offsets_of(counts), sum(counts)
+        X, dY = tokens(T, T, K), tokens(T + 1, T, N, 0.01)
+        Y, dX = q.qlora_int8_expert_fwd(X, w, off), q.qlora_int8_expert_bwd(dY, w, off)
+        for e, s in ((0, slice(0, counts[0])), (E - 1, slice(counts[0], T))):
+            we = q.Int8Rows(w.codes[e], w.scale[e], (N, K))
+            ref.check_forward(Y[s], fwd_ref(X[s], we), f"expert {e}")
+            ref.check_backward(dX[s], dY[s], compute_weight(we), f"expert {e}")
+    assert q.qlora_device_error() == 0
