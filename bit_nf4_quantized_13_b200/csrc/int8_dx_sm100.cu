@@ -207,10 +207,13 @@ __device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb,
     for (int it = P.pair; it < items.count; it += P.num_pairs) {
         const Item x = item_of(p.q, tb, items, it);
         const float* scale = p.scale + static_cast<int64_t>(x.tl.expert) * p.N;
+        // rows past N hold other codes or zeros: scale 0 makes them 0
+        int n = (x.kb0 + kb) * kBK + (quarter & 1) * 32 + lane;
+        float next = n < p.N ? __ldg(scale + n) : 0.0f;
         for (; kb < x.stages; kb += kParts) {
-            // rows past N hold other codes or zeros: scale 0 makes them 0
-            const int n = (x.kb0 + kb) * kBK + (quarter & 1) * 32 + lane;
-            const float mine = n < p.N ? __ldg(scale + n) : 0.0f;
+            const float mine = next;
+            n += kParts * kBK;  // the scales of this part's next stage, on their way meanwhile
+            next = n < p.N ? __ldg(scale + n) : 0.0f;
             if (!warp_wait(P.raw_full(raw.slot), raw.turn)) return;
             const uint32_t src = P.sRaw(raw.slot) + src0;
             uint4 cb[4];
