@@ -93,18 +93,17 @@ struct Maps {
 struct Pipe {
     uint32_t smem, bar0, tmem, rank;
     int pair, num_pairs;
-    __device__ uint32_t full_b(int s) const { return bar0 + 8u * s; }
-    __device__ uint32_t full_a(int s) const { return bar0 + 8u * (kStages + s); }
-    __device__ uint32_t empty(int s) const { return bar0 + 8u * (2 * kStages + s); }
-    __device__ uint32_t raw_full(int s) const { return bar0 + 8u * (3 * kStages + s); }
-    __device__ uint32_t raw_empty(int s) const { return bar0 + 8u * (3 * kStages + kRaw + s); }
-    __device__ uint32_t acc_full(int b) const { return bar0 + 8u * (3 * kStages + 2 * kRaw + b); }
-    __device__ uint32_t acc_empty(int b) const { return bar0 + 8u * (3 * kStages + 2 * kRaw + 2 + b); }
-    __device__ uint32_t drain() const { return bar0 + 8u * (3 * kStages + 2 * kRaw + 4); }
+    __device__ uint32_t full(int s) const { return bar0 + 8u * s; }
+    __device__ uint32_t empty(int s) const { return bar0 + 8u * (kStages + s); }
+    __device__ uint32_t raw_full(int s) const { return bar0 + 8u * (2 * kStages + s); }
+    __device__ uint32_t raw_empty(int s) const { return bar0 + 8u * (2 * kStages + kRaw + s); }
+    __device__ uint32_t acc_full(int b) const { return bar0 + 8u * (2 * kStages + 2 * kRaw + b); }
+    __device__ uint32_t acc_empty(int b) const { return bar0 + 8u * (2 * kStages + 2 * kRaw + 2 + b); }
+    __device__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + 2 * kRaw + 4); }
     __device__ uint32_t sA(int s) const { return smem + static_cast<uint32_t>(s * kStageBytes); }
     __device__ uint32_t sRaw(int s) const { return smem + static_cast<uint32_t>(kRawOff + s * kRawBytes); }
 };
-constexpr int kBars = 3 * kStages + 2 * kRaw + 5;
+constexpr int kBars = 2 * kStages + 2 * kRaw + 5;
 static_assert(8 * kBars + 8 <= kTableOff - kBarOff, "barriers and the TMEM address");
 
 // A position in a ring of kSlots, with the parity of its turn.
@@ -131,8 +130,8 @@ __device__ void role_tokens(const Pipe& P, const Params& p, const RowTable& tb, 
         const uint32_t tx = 2u * static_cast<uint32_t>(box_rows(box) * kBK * 2);
         for (int kb = x.kb0; kb < x.kb0 + x.stages; ++kb, ring.step(1)) {
             if (!mbar_wait(P.empty(ring.slot), ring.turn, &g_int8_dx_error)) return;
-            if (P.rank == 0) mbar_arrive_expect_tx(P.full_b(ring.slot), tx);
-            tma_load_2d_pair(P.sA(ring.slot) + kABytes, &maps.y[box], cluster_map(P.full_b(ring.slot), 0), kb * kBK, row);
+            if (P.rank == 0) mbar_arrive_expect_tx(P.full(ring.slot), tx);
+            tma_load_2d_pair(P.sA(ring.slot) + kABytes, &maps.y[box], cluster_map(P.full(ring.slot), 0), kb * kBK, row);
         }
     }
 }
@@ -167,8 +166,7 @@ __device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, con
         if (!mbar_wait(P.acc_empty(b), (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u, &g_int8_dx_error)) return;
         tc_fence_after();
         for (int kb = 0; kb < x.stages; ++kb, ring.step(1)) {
-            if (!mbar_wait(P.full_b(ring.slot), ring.turn, &g_int8_dx_error)) return;
-            if (!mbar_wait(P.full_a(ring.slot), ring.turn, &g_int8_dx_error)) return;
+            if (!mbar_wait(P.full(ring.slot), ring.turn, &g_int8_dx_error)) return;
             tc_fence_after();
             const uint64_t off = static_cast<uint64_t>(ring.slot) * (kStageBytes / 16);
 #pragma unroll
@@ -197,7 +195,7 @@ __device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb,
     const int q = lane >> 3;
     const int r = (lane & 4) ? q ^ 5 : q;           // row within 8
     const int row0 = (quarter & 1) * 32 + r;        // + 8 j: this lane's rows of the stage
-    const uint32_t full_a0 = cluster_map(P.full_a(part), 0);
+    const uint32_t full0 = cluster_map(P.full(part), 0);
     const uint32_t src0 = static_cast<uint32_t>(row0 * 128 + (((panel * 4 + c) ^ r) << 4));
     const uint32_t dst = P.sA(part) + static_cast<uint32_t>(panel * kPanelBytes + row0 * 128);
     const uint32_t dst0 = dst + (((2 * c) ^ r) << 4), dst1 = dst + (((2 * c + 1) ^ r) << 4);
@@ -244,7 +242,7 @@ __device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb,
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(full_a0);
+            if (lane == 0) mbar_arrive_remote(full0);
         }
         kb -= x.stages;
     }
@@ -300,9 +298,8 @@ k_int8_dx_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params
     P.num_pairs = static_cast<int>(gridDim.x >> 1);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(P.full_b(s), 1);      // the even CTA's expect_tx arrival (+ both CTAs' bytes)
-            mbar_init(P.full_a(s), 2 * 4);  // the part's four warps in each CTA
-            mbar_init(P.empty(s), 1);       // the pair MMA's commit
+            mbar_init(P.full(s), 1 + 2 * 4);  // the even CTA's expect_tx (+ both CTAs' bytes), the part's warps in each CTA
+            mbar_init(P.empty(s), 1);         // the pair MMA's commit
         }
         for (int s = 0; s < kRaw; ++s) {
             mbar_init(P.raw_full(s), 1);    // this CTA's expect_tx arrival (+ its bytes)
