@@ -82,6 +82,7 @@ struct Params {
     const float* scale;  // E x N
     Schedule q;          // column tiles: ceil(K / 256); stages: ceil(N / 64)
     int N, K;
+    int boxes;           // token maps made
     uint16_t* dX;
 };
 
@@ -318,7 +319,7 @@ k_int8_dx_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params
     }
     if (warp == 1 && lane == 0) {
         tma_prefetch_desc(&maps.w);
-        for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.y[i]);
+        for (int i = 0; i < p.boxes; ++i) tma_prefetch_desc(&maps.y[i]);
     }
     if (warp == 2) build_table(p.q, tb, lane);
     tc_fence_before();
@@ -472,10 +473,11 @@ cudaError_t launch_int8_dx(const uint16_t* dY, const Int8Weight& w, const RowRan
     if (parts_bytes(rr.T, w) > 0) p.q.slots = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + padded_bytes(rr.T, w));
     p.N = static_cast<int>(w.N);
     p.K = static_cast<int>(w.K);
+    p.boxes = boxes_of(p.q);
     p.dX = dX;
     Maps maps;
     bool ok = make_map(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.K, w.E * w.N, w.ld, kRowsCta, kBK);
-    for (int i = 0; i < kBoxes; ++i)
+    for (int i = 0; i < p.boxes; ++i)
         ok = ok && make_map(&maps.y[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dY, w.N, rr.T, ldy * 2, kBK,
                             static_cast<uint32_t>(box_rows(i)));
     if (!ok) return cudaErrorInvalidValue;

@@ -271,10 +271,15 @@ inline cudaLaunchConfig_t add_config(cudaLaunchAttribute (&attr)[1], const Sched
 
 // The MMA's width for a tile's tokens, and the token rows each CTA of the
 // pair copies for it (half of them, in a box of 32, 64 or 128 rows).
-__device__ __forceinline__ int mma_tokens(int toks) { return (toks + 31) & ~31; }
-__device__ __forceinline__ int box_index(int half) { return half > 64 ? 2 : half > 32 ? 1 : 0; }
+__host__ __device__ constexpr int mma_tokens(int toks) { return (toks + 31) & ~31; }
+__host__ __device__ constexpr int box_index(int half) { return half > 64 ? 2 : half > 32 ? 1 : 0; }
 constexpr int kBoxes = 3;
 __host__ __device__ constexpr int box_rows(int i) { return 32 << i; }
+// The boxes that a schedule's tiles can need: the first ones.  The others' maps
+// are not made (each takes the host part of a microsecond).
+inline int boxes_of(const Schedule& q) {
+    return box_index(mma_tokens(q.rr.T < q.cap ? static_cast<int>(q.rr.T) : q.cap) / 2) + 1;
+}
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t r;
