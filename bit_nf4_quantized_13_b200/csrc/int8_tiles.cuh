@@ -1,6 +1,7 @@
 // int8_tiles.cuh -- what the Int8 linear's two tensor-core products share: the
-// tiles of ragged row ranges (dense: one range), and the bf16 store of a
-// transposed accumulator.
+// tiles of ragged row ranges (dense: one range) and their schedule, the parts of
+// tiles cut along the contraction, the conversion of codes and the bf16 store of
+// a transposed accumulator.
 #pragma once
 
 #include "common.cuh"

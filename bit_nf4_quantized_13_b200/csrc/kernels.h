@@ -74,10 +74,10 @@ __device__ __forceinline__ void expert_rows(const RowRanges& rr, int e, int* lo,
 // stream is the row quantizer, which it may overlap.
 int64_t int8_tiles(int64_t T, int E, int64_t w_rows, int tile_tok);
 bool int8_pair_supported(int64_t T, const Int8Weight& w);
+size_t int8_pair_workspace(int64_t T, const Int8Weight& w);  // the sums of tiles that are cut along the contraction
 cudaError_t launch_int8_fwd_pair(const int8_t* x_codes, const float* x_scale, const Int8Weight& w,
                                  const RowRanges& rr, void* out, int out_dtype, void* ws, cudaStream_t stream,
                                  bool dependent);
-size_t int8_pair_workspace(int64_t T, const Int8Weight& w);
 int int8_device_error(int reset);
 
 // int8_gemv.cu -- the forward for a few tokens, by streaming the weights.
@@ -89,7 +89,8 @@ cudaError_t launch_int8_fwd_gemv(const uint16_t* X, const int8_t* x_codes, const
                                  const RowRanges& rr, void* out, int out_dtype, cudaStream_t stream, bool dependent);
 
 // int8_dx_sm100.cu -- the input gradient on the tensor cores, on pairs of SMs.
-// Workspace: dY's rows padded to 16 bytes, where N is not a multiple of 8.
+// Workspace: dY's rows padded to 16 bytes, where N is not a multiple of 8, and
+// the sums of tiles that are cut along the contraction.
 bool int8_dx_supported(int64_t T, const Int8Weight& w);
 size_t int8_dx_workspace(int64_t T, const Int8Weight& w);
 cudaError_t launch_int8_dx(const uint16_t* dY, const Int8Weight& w, const RowRanges& rr, uint16_t* dX, void* ws,
