@@ -4,6 +4,8 @@
 #include <atomic>
 #include <mutex>
 
+#include <initializer_list>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -383,6 +385,21 @@ int qlora_int8_dequantize(const int8_t* codes, const float* c, int64_t numel, in
 // ---- the Int8 linear, dense (offsets == nullptr, E = 1) or by expert
 namespace {
 
+// An array of a call; an output must not overlap another one (its kernels read
+// their inputs while other blocks write).
+struct Span {
+    const void* p;
+    int64_t bytes;
+};
+bool overlaps(const Span& out, std::initializer_list<Span> others) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(out.p);
+    for (const Span& o : others) {
+        const uintptr_t b = reinterpret_cast<uintptr_t>(o.p);
+        if (o.p && a < b + static_cast<uintptr_t>(o.bytes) && b < a + static_cast<uintptr_t>(out.bytes)) return true;
+    }
+    return false;
+}
+
 int check_int8(int64_t T, int E, int64_t N, int64_t K, bool by_expert, const int32_t* offsets) {
     if (T < 0 || E < 1 || N < 1 || K < 1) return QLORA_ERR_INVALID_ARG;
     if (by_expert && T > 0 && !ok_ptr(offsets)) return QLORA_ERR_INVALID_ARG;
@@ -425,6 +442,12 @@ int int8_fwd(const uint16_t* X, const int8_t* x_codes, const float* x_scale, con
     const RowRanges rr{offsets, T};
     const bool few = int8_gemv_pays(T, w);
     if (!few && !int8_pair_supported(T, w)) return QLORA_ERR_UNSUPPORTED;
+    const Span x = quantized ? Span{x_codes, T * w.ld} : Span{X, T * K * 2}, xs = {quantized ? x_scale : nullptr, T * 4};
+    const Span wc = {w_codes, E * N * w.ld}, wsc = {w_scale, E * N * 4}, off = {offsets, (E + 1) * 4};
+    const Span scratch = {ws, static_cast<int64_t>(need)};
+    if (overlaps({Y, T * N * (out_dtype == 0 ? 4 : 2)}, {x, xs, wc, wsc, off, scratch}) ||
+        overlaps(scratch, {x, xs, wc, wsc, off}))
+        return QLORA_ERR_INVALID_ARG;
     cudaStream_t cs = as_stream(stream);
     if (!quantized && int8_gemv_fused(T, w))
         return cuda_status(launch_int8_fwd_gemv(X, nullptr, nullptr, w, rr, Y, out_dtype, cs, false));
@@ -453,6 +476,10 @@ int int8_bwd(const uint16_t* dY, const int32_t* offsets, bool by_expert, int64_t
     if (need > 0 && (!ws || !aligned16(ws) || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
     const Int8Weight w{w_codes, w_scale, E, N, K, int8_row_bytes(K)};
     if (!int8_dx_supported(T, w)) return QLORA_ERR_UNSUPPORTED;
+    const Span dy = {dY, T * N * 2}, wc = {w_codes, E * N * w.ld}, wsc = {w_scale, E * N * 4}, off = {offsets, (E + 1) * 4};
+    const Span scratch = {ws, static_cast<int64_t>(need)};
+    if (overlaps({dX, T * K * 2}, {dy, wc, wsc, off, scratch}) || overlaps(scratch, {dy, wc, wsc, off}))
+        return QLORA_ERR_INVALID_ARG;
     return pair_status(launch_int8_dx(dY, w, RowRanges{offsets, T}, dX, ws, as_stream(stream)));
 }
 
@@ -467,6 +494,10 @@ int qlora_int8_quantize_rows(const void* x, int x_dtype, int64_t rows, int64_t K
     if (status && (reinterpret_cast<uintptr_t>(status) & 3u)) return QLORA_ERR_INVALID_ARG;
     if (rows == 0) return QLORA_OK;
     if (!ok_ptr(x) || !ok_ptr(codes) || !ok_ptr(scale)) return QLORA_ERR_INVALID_ARG;
+    const Span in = {x, rows * K * (x_dtype == 0 ? 4 : 2)}, sc = {scale, rows * 4}, st = {status, 4};
+    if (overlaps({codes, rows * int8_row_bytes(K)}, {in, sc, st}) || overlaps(sc, {in, st}) ||
+        (status && overlaps(st, {in})))
+        return QLORA_ERR_INVALID_ARG;
     return cuda_status(launch_int8_rows(x, x_dtype, rows, K, codes, scale, status, as_stream(stream)));
 }
 

@@ -347,7 +347,8 @@ int qlora_int8_dequantize(const int8_t* codes, const float* c, int64_t numel, in
  *
  * Rows of codes are QLORA_INT8_ROW_BYTES(K) bytes apart: K codes, then zero
  * codes up to a multiple of 16 bytes.  K <= QLORA_INT8_MAX_K keeps every
- * 32-bit sum of products exact.
+ * 32-bit sum of products exact.  An output or workspace that overlaps another
+ * array of its call is refused (QLORA_ERR_INVALID_ARG).
  * --------------------------------------------------------------------- */
 #define QLORA_INT8_ROW_BYTES(K) (((K) + 15) / 16 * 16)
 #define QLORA_INT8_MAX_K 131072

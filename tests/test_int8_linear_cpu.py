@@ -82,6 +82,26 @@ def test_expert_refusals(lib):
     assert f(P, P, 0, 2, 8, 8, P, P, None, None, 0, None) == OK
 
 
+def test_overlapping_arrays_are_refused(lib):
+    A = [(i + 1) << 40 for i in range(7)]  # far apart; every call below has one overlap and is refused for it
+    X, W, S, Y, WS, O, XS = A
+    T, N, K = 40, 64, 96
+    f = lib.qlora_int8_linear_fwd
+    for y, ws in ((X, WS), (X + T * K * 2 - 16, WS), (W + 16, WS), (S, WS), (WS, WS), (Y, Y), (Y, X), (Y, W), (Y, S),
+                  (X - T * N * 2 + 16, WS)):
+        assert f(X, T, N, K, W, S, y, 1, ws, 1 << 30, None) == INVALID
+    assert f(X, 2, N, K, W, S, X, 1, None, 0, None) == INVALID  # one kernel, no workspace
+    assert lib.qlora_int8_matmul(X, XS, T, N, K, W, S, XS, 1, WS, 1 << 30, None) == INVALID
+    assert lib.qlora_int8_expert_fwd(X, O, T, 2, N, K, W, S, O, 1, WS, 1 << 30, None) == INVALID
+    f = lib.qlora_int8_linear_bwd
+    for n, dx, ws in ((N, X, WS), (N, W, WS), (N, S, WS), (63, Y, X), (63, Y, Y), (63, Y, W)):
+        assert f(X, T, n, K, W, S, dx, ws, 1 << 30, None) == INVALID
+    f = lib.qlora_int8_quantize_rows
+    for codes, scale, status in ((X, S, None), (X + T * K * 2 - 16, S, None), (W, W, None), (W, X, None), (W, S, W),
+                                 (W, S, S), (W, S, X)):
+        assert f(X, 1, T, K, codes, scale, status, None) == INVALID
+
+
 def test_workspace_sizes(lib):
     # the tokens' codes (rows of 16-byte multiples) and scales at least
     assert q.qlora_int8_linear_fwd_workspace_size(100, 8, 33) >= 100 * 48 + 400
