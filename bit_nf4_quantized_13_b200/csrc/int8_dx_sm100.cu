@@ -80,7 +80,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kRawOff = kStages * kStageBytes;
 constexpr int kBarOff = kRawOff + kRaw * kRawBytes;
 constexpr int kTableOff = kBarOff + 512;
-constexpr int kSmemBytes = 1024 /* alignment slack */ + kTableOff + kRowTableBytes;
+constexpr int kSmemBytes = 1024 /* alignment slack */ + kTableOff + kRowTableBytes + kItemListBytes;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 constexpr uint16_t kPairMask = 0x3;
 
@@ -100,6 +100,7 @@ struct Maps {
 struct Pipe {
     uint32_t smem, bar0, tmem, rank;
     int pair, num_pairs;
+    Item* list;
     __device__ uint32_t full(int s) const { return bar0 + 8u * s; }
     __device__ uint32_t empty(int s) const { return bar0 + 8u * (kStages + s); }
     __device__ uint32_t raw_full(int s) const { return bar0 + 8u * (2 * kStages + s); }
@@ -129,8 +130,8 @@ struct Ring {
 
 __device__ void role_tokens(const Pipe& P, const Params& p, const RowTable& tb, const Items& items, const Maps& maps) {
     Ring<kStages> ring{0, 1};
-    for (int it = P.pair; it < items.count; it += P.num_pairs) {
-        const Item x = item_of(p.q, tb, items, it);
+    for (int i = 0, it = P.pair; it < items.count; it += P.num_pairs, ++i) {
+        const Item x = listed_item(p.q, tb, items, P.list, i, it);
         const Tile& tl = x.tl;
         const int half = mma_tokens(tl.toks) / 2, box = box_index(half);
         const int row = tl.tok0 + static_cast<int>(P.rank) * half;
@@ -145,8 +146,8 @@ __device__ void role_tokens(const Pipe& P, const Params& p, const RowTable& tb, 
 
 __device__ void role_codes(const Pipe& P, const Params& p, const RowTable& tb, const Items& items, const Maps& maps) {
     Ring<kRaw> ring{0, 1};
-    for (int it = P.pair; it < items.count; it += P.num_pairs) {
-        const Item x = item_of(p.q, tb, items, it);
+    for (int i = 0, it = P.pair; it < items.count; it += P.num_pairs, ++i) {
+        const Item x = listed_item(p.q, tb, items, P.list, i, it);
         const int col = x.tl.row0 + static_cast<int>(P.rank) * kRowsCta, n0 = x.tl.expert * p.N;
         for (int kb = x.kb0; kb < x.kb0 + x.stages; ++kb, ring.step(1)) {
             if (!mbar_wait(P.raw_empty(ring.slot), ring.turn, &g_int8_dx_error)) return;
@@ -167,7 +168,7 @@ __device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, con
     Ring<kStages> ring{0, 0};
     int i = 0;
     for (int it = P.pair; it < items.count; it += P.num_pairs, ++i) {
-        const Item x = item_of(p.q, tb, items, it);
+        const Item x = listed_item(p.q, tb, items, P.list, i, it);
         const uint32_t idesc = idesc_bf16(kTileRows, mma_tokens(x.tl.toks), 1, 0);
         const int b = i & 1;
         if (!mbar_wait(P.acc_empty(b), (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u, &g_int8_dx_error)) return;
@@ -209,8 +210,8 @@ __device__ void role_convert(const Pipe& P, const Params& p, const RowTable& tb,
     Ring<kRaw> raw{part, 0};
     uint32_t turn = 1;
     int kb = part;  // this part's next stage, counted from the item's first
-    for (int it = P.pair; it < items.count; it += P.num_pairs) {
-        const Item x = item_of(p.q, tb, items, it);
+    for (int i = 0, it = P.pair; it < items.count; it += P.num_pairs, ++i) {
+        const Item x = listed_item(p.q, tb, items, P.list, i, it);
         const float* scale = p.scale + static_cast<int64_t>(x.tl.expert) * p.N;
         // rows past N hold other codes or zeros: scale 0 makes them 0
         int n = (x.kb0 + kb) * kBK + (quarter & 1) * 32 + lane;
@@ -268,7 +269,7 @@ __device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     int i = 0;
     for (int it = P.pair; it < items.count; it += P.num_pairs, ++i) {
-        const Item x = item_of(p.q, tb, items, it);
+        const Item x = listed_item(p.q, tb, items, P.list, i, it);
         const int b = i & 1, row = quarter * 32 + lane;
         if (!warp_wait(P.acc_full(b), static_cast<uint32_t>(i >> 1) & 1u)) return;
         tc_fence_after();
@@ -335,6 +336,9 @@ k_int8_dx_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params
     tc_fence_after();
     P.tmem = *tmem_slot;
     const Items items = items_of(p.q, tb);
+    P.list = reinterpret_cast<Item*>(smem + kTableOff + kRowTableBytes);
+    list_items(p.q, tb, items, P.pair, P.num_pairs, P.list);
+    __syncthreads();
     grid_dependency_wait();  // dY's padded rows
     if (warp == 0) {
         if (elect_one()) role_tokens(P, p, tb, items, maps);

@@ -59,7 +59,7 @@ constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr int kBarOff = kRingBytes;
 constexpr int kTableOff = kBarOff + 256;
-constexpr int kSmemBytes = 1024 /* alignment slack */ + kTableOff + kRowTableBytes;
+constexpr int kSmemBytes = 1024 /* alignment slack */ + kTableOff + kRowTableBytes + kItemListBytes;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 constexpr uint16_t kPairMask = 0x3;
 
@@ -92,6 +92,7 @@ struct Maps {
 struct Pipe {
     uint32_t smem, bar0, tmem, rank;
     int pair, num_pairs;
+    Item* list;
     __device__ uint32_t full(int s) const { return bar0 + 8u * s; }
     __device__ uint32_t empty(int s) const { return bar0 + 8u * (kMaxStages + s); }
     __device__ uint32_t acc_full(int b) const { return bar0 + 8u * (2 * kMaxStages + b); }
@@ -102,8 +103,8 @@ struct Pipe {
 __device__ void role_tma(const Pipe& P, const Params& p, const RowTable& tb, const Items& items, const Maps& maps) {
     int s = 0;
     uint32_t ph = 1;
-    for (int it = P.pair; it < items.count; it += P.num_pairs) {
-        const Item x = item_of(p.q, tb, items, it);
+    for (int i = 0, it = P.pair; it < items.count; it += P.num_pairs, ++i) {
+        const Item x = listed_item(p.q, tb, items, P.list, i, it);
         const Tile& tl = x.tl;
         const int half = mma_tokens(tl.toks) / 2;
         const int box = box_index(half);
@@ -138,7 +139,7 @@ __device__ void role_mma(const Pipe& P, const Params& p, const RowTable& tb, con
     int s = 0, i = 0;
     uint32_t ph = 0;
     for (int it = P.pair; it < items.count; it += P.num_pairs, ++i) {
-        const Item x = item_of(p.q, tb, items, it);
+        const Item x = listed_item(p.q, tb, items, P.list, i, it);
         const int b = i & 1;
         const uint32_t idesc = idesc_i8(kRowsPair, mma_tokens(x.tl.toks));
         if (!mbar_wait(P.acc_empty(b), (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u, &g_int8_error)) return;
@@ -198,7 +199,7 @@ __device__ void role_epilogue(const Pipe& P, const Params& p, const RowTable& tb
     float* sx = s_sx[warp - 2];
     int i = 0;
     for (int it = P.pair; it < items.count; it += P.num_pairs, ++i) {
-        const Item x = item_of(p.q, tb, items, it);
+        const Item x = listed_item(p.q, tb, items, P.list, i, it);
         const Tile& tl = x.tl;
         const int b = i & 1;
         const int chunks = mma_tokens(tl.toks) / 32;
@@ -274,6 +275,9 @@ k_int8_gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Para
     tc_fence_after();
     P.tmem = *tmem_slot;
     const Items items = items_of(p.q, tb);
+    P.list = reinterpret_cast<Item*>(smem + kTableOff + kRowTableBytes);
+    list_items(p.q, tb, items, P.pair, P.num_pairs, P.list);
+    __syncthreads();
     grid_dependency_wait();  // the quantized tokens
     if (warp == 0) {
         if (elect_one()) role_tma(P, p, tb, items, maps);

@@ -17,7 +17,7 @@ struct RowTable {
     int* off;    // E + 1: expert e's rows are [off[e], off[e + 1]), ascending in [0, T]
     int* tile0;  // E + 1: tiles of the experts before e; tile0[E]: all tiles
 };
-constexpr int kRowTableBytes = 2 * 4 * (QLORA_MAX_EXPERTS + 1);
+constexpr int kRowTableBytes = (2 * 4 * (QLORA_MAX_EXPERTS + 1) + 15) / 16 * 16;
 
 __device__ __forceinline__ RowTable row_table(void* smem) {
     return RowTable{static_cast<int*>(smem), static_cast<int*>(smem) + QLORA_MAX_EXPERTS + 1};
@@ -150,7 +150,7 @@ __device__ __forceinline__ Items items_of(const Schedule& q, const RowTable& tb)
 }
 
 // One item: a tile, or a part of one.
-struct Item {
+struct alignas(16) Item {
     Tile tl;
     int kb0, stages;
     int slot;  // -1: the whole tile
@@ -172,6 +172,22 @@ __device__ __forceinline__ Item item_of(const Schedule& q, const RowTable& tb, c
     }
     x.tl = tile_of(q, tb, tile);
     return x;
+}
+
+// A pair's first items, worked out once by a thread each: every warp asks for
+// every item, and the search and divisions of item_of would cost each of them
+// some 400 cycles a tile, against 4000 to 9000 of a tile of 16 stages.
+constexpr int kListed = 64;
+constexpr int kItemListBytes = kListed * static_cast<int>(sizeof(Item));
+__device__ __forceinline__ void list_items(const Schedule& q, const RowTable& tb, const Items& items, int pair, int pairs,
+                                           Item* list) {
+    for (int i = threadIdx.x; i < kListed && pair + i * pairs < items.count; i += blockDim.x)
+        list[i] = item_of(q, tb, items, pair + i * pairs);
+}
+// The pair's i-th item, `it` of all.
+__device__ __forceinline__ Item listed_item(const Schedule& q, const RowTable& tb, const Items& items, const Item* list,
+                                            int i, int it) {
+    return i < kListed ? list[i] : item_of(q, tb, items, it);
 }
 
 // A slot holds [CTA][chunk of 32 tokens][group of 4 tokens][row][4], so that
