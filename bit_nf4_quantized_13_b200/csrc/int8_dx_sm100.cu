@@ -75,6 +75,11 @@ constexpr int kRawBytes = kBK * kRowsCta;  // 8 KiB of codes
 constexpr int kConvWarp0 = 4, kConvWarps = 16, kEpiWarp0 = kConvWarp0 + kConvWarps;
 constexpr int kParts = kConvWarps / 4;
 static_assert(kParts == kStages, "a part's stages must always use the same ring slot");
+// A part waits for the codes of stage i + kParts once it has stored stage i, that
+// is when the MMAs of stage i - kStages are done.  By then the use of the slot
+// before, stage i + kParts - kRaw, must be over: else its predecessor's parity
+// would be taken for the one waited for.
+static_assert(kRaw >= kStages + kParts, "the codes' ring");
 constexpr int kThreads = 32 * (kEpiWarp0 + 4);
 constexpr uint32_t kTmemCols = 512;
 constexpr int kRawOff = kStages * kStageBytes;
