@@ -23,12 +23,12 @@
 //   warps 20-23  epilogue of the TMEM lane quarter w % 4, under the next tile's
 //                stages (two accumulators)
 //
-// A stage takes about 490 cycles with few tokens and 680 to 750 with 256, where
+// A stage takes 500 to 570 cycles with few tokens and 680 to 750 with 256, where
 // its MMAs take 156 and 512: 4096 x 11008 x 4096 takes 241 us (tensor pipe 86%
-// active), 1500 rows over 64 experts of 1024 x 2048 50 us (137 MB, 22 us at the
-// copy rate).  Cycle counters: of a converter warp's 2450 a turn (four stages)
-// loading and converting takes 800, storing and the proxy fence 550, waiting for
-// the slot 600; the shared memory's 88 KiB a stage alone are 690 cycles at 256
+// active), 1500 rows over 64 experts of 1024 x 2048 48 us (137 MB, 22 us at the
+// copy rate).  Cycle counters: of a converter warp's 2450 a turn (one stage in
+// four) loading and converting takes 800, storing and the proxy fence 550,
+// waiting for the slot 600; the shared memory's 88 KiB a stage alone are 690 cycles at 256
 // tokens.  Without the arithmetic 706 of 752 remain.  Tried and slower: the
 // weights through tensor memory (no shared-memory operand, but 500 to 600 cycles
 // a stage of 128 to 192 tokens), tiles of 512 tokens with codes loaded through
