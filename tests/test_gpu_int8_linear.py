@@ -3,6 +3,11 @@ output channel) and of its expert-grouped form against their definitions in
 64 bits: codes, scales and untouched rows bit for bit, products within the
 counted roundings.  Sizes from one row to several tiles, ragged row ranges,
 masked (empty) experts, non-finite rows, streams and captured graphs."""
+import os
+import subprocess
+import sys
+import threading
+
 import pytest
 import torch
 
@@ -475,3 +480,56 @@ def test_offsets_past_32_bits():
             ref.check_forward(Y[s], fwd_ref(X[s], we), f"expert {e}")
             ref.check_backward(dX[s], dY[s], compute_weight(we), f"expert {e}")
     assert q.qlora_device_error() == 0
+
+
+def test_threads_on_their_own_streams():
+    N, K, sizes = 300, 640, (400, 2, 64, 200)
+    X, dY, w = tokens(1, 400, K), tokens(2, 400, N, 0.01), weight(3, N, K)
+    want = {m: (q.qlora_int8_linear_fwd(X[:m], w), q.qlora_int8_linear_bwd(dY[:m], w)) for m in sizes}
+    torch.cuda.synchronize()
+    got = {}
+
+    def run(k):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            outs = []
+            for i in range(40):
+                m = sizes[(i + k) % 4]
+                outs.append((m, q.qlora_int8_linear_fwd(X[:m], w), q.qlora_int8_linear_bwd(dY[:m], w)))
+            stream.synchronize()
+        got[k] = outs
+
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert sorted(got) == [0, 1, 2, 3]
+    for outs in got.values():
+        for m, Y, dX in outs:
+            assert torch.equal(Y, want[m][0]) and torch.equal(dX, want[m][1])
+
+
+FIRST_CALLS_CAPTURED = """
+import torch, bit_nf4_quantized_13_b200 as q
+w = q.qlora_int8_quantize_rows(torch.randn(2, 300, 640, device="cuda"))
+X = torch.randn(400, 640, device="cuda").bfloat16()
+dY = torch.randn(400, 300, device="cuda").bfloat16()
+off = torch.tensor([0, 100, 400], dtype=torch.int32, device="cuda")
+graph = torch.cuda.CUDAGraph()
+def calls():
+    return (q.qlora_int8_expert_fwd(X, w, off), q.qlora_int8_expert_fwd(X[:3], w, off), q.qlora_int8_expert_fwd(X[:12], w, off),
+            q.qlora_int8_expert_bwd(dY, w, off), q.qlora_int8_quantize_rows(X).codes)
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, calls()))
+assert q.qlora_device_error() == 0
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
