@@ -94,6 +94,7 @@ def _load() -> ctypes.CDLL:
         "qlora_int8_expert_fwd": (i32, [vp, vp, i64, i32, i64, i64, vp, vp, vp, i32, vp, sz, vp]),
         "qlora_int8_expert_matmul": (i32, [vp, vp, vp, i64, i32, i64, i64, vp, vp, vp, i32, vp, sz, vp]),
         "qlora_int8_expert_bwd": (i32, [vp, vp, i64, i32, i64, i64, vp, vp, vp, vp, sz, vp]),
+        "qlora_int8_expert_zero_rows": (i32, [vp, i64, i32, i64, i32, vp, vp]),
         "qlora_debug_fill": (i32, [vp, i64, ctypes.c_uint32, vp]),
         "qlora_debug_read": (i32, [vp, i64, ctypes.c_uint32, vp, vp]),
         "qlora_linear_group_fwd_workspace_size": (sz, [i64, i32, i32]),
@@ -677,6 +678,13 @@ def _int8_buffers(out, shape, dtype, ws, need, like, stream):
     return out, ws
 
 
+def _int8_zero_rows(out, offsets, code, stream):
+    """A new output's rows of no expert, which the product leaves as they are."""
+    _check("qlora_int8_expert_zero_rows",
+           _get_lib().qlora_int8_expert_zero_rows(offsets.data_ptr(), out.shape[0], offsets.numel() - 1, out.shape[1],
+                                                  code, out.data_ptr(), _stream(stream)))
+
+
 def _int8_fwd(X, w, offsets, out_dtype, Y, ws, stream):
     torch, lib = _torch(), _get_lib()
     T, E, N, K = _int8_dims(X, w, offsets, False)
@@ -698,7 +706,10 @@ def _int8_fwd(X, w, offsets, out_dtype, Y, ws, stream):
     else:
         fn = "qlora_int8_expert_matmul" if quantized else "qlora_int8_expert_fwd"
         sizes = (T, E, N, K)
+    made = Y is None
     Y, ws = _int8_buffers(Y, (T, N), out_dtype, ws, getattr(lib, fn + "_workspace_size")(*sizes), wsc, stream)
+    if made and offsets is not None:
+        _int8_zero_rows(Y, offsets, code, stream)
     # addresses go as plain integers: a ctypes object for each costs more than the checks of a call
     st = getattr(lib, fn)(*[t.data_ptr() for t in x], *(() if offsets is None else (offsets.data_ptr(),)), *sizes,
                           wc.data_ptr(), wsc.data_ptr(), Y.data_ptr(), code, None if ws is None else ws.data_ptr(),
@@ -717,7 +728,10 @@ def _int8_bwd(dY, w, offsets, dX, ws, stream):
     _need_cuda(dY, w.codes, w.scale, offsets, dX, ws)
     need = (lib.qlora_int8_linear_bwd_workspace_size(T, N, K) if offsets is None
             else lib.qlora_int8_expert_bwd_workspace_size(T, E, N, K))
+    made = dX is None
     dX, ws = _int8_buffers(dX, (T, K), torch.bfloat16, ws, need, dY, stream)
+    if made and offsets is not None:
+        _int8_zero_rows(dX, offsets, 1, stream)
     tail = (w.codes.data_ptr(), w.scale.data_ptr(), dX.data_ptr(), None if ws is None else ws.data_ptr(),
             0 if ws is None else ws.numel(), _stream(stream))
     if offsets is None:
@@ -745,14 +759,16 @@ def qlora_int8_linear_bwd(dY, w: Int8Rows, dX=None, ws=None, stream=None):
 def qlora_int8_expert_fwd(X, w: Int8Rows, offsets, out_dtype=None, Y=None, ws=None, stream=None):
     """qlora_int8_linear_fwd by expert: rows offsets[e] .. offsets[e + 1] - 1
     of X use the weight w[e] (w: E x N x K; offsets: int32 [E + 1] on the
-    device).  Rows outside every range keep what Y held."""
+    device).  Rows outside every range keep what Y held; they are zeros where
+    the call makes Y."""
     if offsets is None:
         raise ValueError("offsets must be an int32 tensor")
     return _int8_fwd(X, w, offsets, out_dtype, Y, ws, stream)
 
 
 def qlora_int8_expert_bwd(dY, w: Int8Rows, offsets, dX=None, ws=None, stream=None):
-    """qlora_int8_linear_bwd by expert, with the rows of qlora_int8_expert_fwd."""
+    """qlora_int8_linear_bwd by expert, with the rows of qlora_int8_expert_fwd
+    (those outside every range keep what dX held, or are zeros in a new dX)."""
     if offsets is None:
         raise ValueError("offsets must be an int32 tensor")
     return _int8_bwd(dY, w, offsets, dX, ws, stream)

@@ -550,6 +550,18 @@ int qlora_int8_expert_bwd(const uint16_t* dY, const int32_t* offsets, int64_t T,
     return int8_bwd(dY, offsets, true, T, E, N, K, w_codes, w_scale, dX, ws, ws_bytes, stream);
 }
 
+int qlora_int8_expert_zero_rows(const int32_t* offsets, int64_t T, int E, int64_t width, int out_dtype, void* out,
+                                void* stream) {
+    if (out_dtype != 0 && out_dtype != 1) return QLORA_ERR_INVALID_ARG;
+    const int st = check_int8(T, E, width, 1, true, offsets);
+    if (st != QLORA_OK) return st;
+    if (T == 0) return QLORA_OK;
+    if (!ok_ptr(out)) return QLORA_ERR_INVALID_ARG;
+    const int64_t row_bytes = width * (out_dtype == 0 ? 4 : 2);
+    if (overlaps({out, T * row_bytes}, {{offsets, (E + 1) * 4}})) return QLORA_ERR_INVALID_ARG;
+    return cuda_status(launch_int8_zero_rows(RowRanges{offsets, T}, E, row_bytes, out, as_stream(stream)));
+}
+
 int qlora_debug_wait_timeout(uint64_t limit_ns, void* stream) {
     if (limit_ns == 0 || limit_ns > kMaxSelftestWaitNs) return QLORA_ERR_INVALID_ARG;
     return cuda_status(launch_wait_selftest(limit_ns, as_stream(stream)));

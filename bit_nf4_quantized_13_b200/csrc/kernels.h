@@ -97,6 +97,10 @@ cudaError_t launch_int8_dx(const uint16_t* dY, const Int8Weight& w, const RowRan
                            cudaStream_t stream);
 int int8_dx_device_error(int reset);
 
+// int8_zero.cu -- zeroes the rows of an expert product's output that belong to
+// no expert (row_bytes even, out 16-byte aligned).
+cudaError_t launch_int8_zero_rows(const RowRanges& rr, int E, int64_t row_bytes, void* out, cudaStream_t stream);
+
 // The frozen NF4 weight W (N x K row-major) as the GEMM kernels see it.
 struct Nf4Weight {
     const uint8_t* codes;   // N*K/2 bytes

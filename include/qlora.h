@@ -430,6 +430,14 @@ int qlora_int8_expert_bwd(const uint16_t* dY, const int32_t* offsets, int64_t T,
                           void* stream);
 
 /*
+ * qlora_int8_expert_zero_rows -- zeroes the rows of `out` (T x width, fp32
+ * (out_dtype 0) or bf16 (1)) that belong to no expert: those the three calls
+ * above leave as they were.  For an output that holds nothing yet.
+ */
+int qlora_int8_expert_zero_rows(const int32_t* offsets, int64_t T, int E, int64_t width, int out_dtype, void* out,
+                                void* stream);
+
+/*
  * qlora_debug_wait_timeout -- failure-detection self-test (no counterpart
  * in the paper).  Launches one single-thread kernel on `stream` whose
  * bounded wait (the same wait every pipeline stage of the tensor-core

@@ -533,3 +533,80 @@ def test_first_calls_of_a_process_may_be_captured():
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+# ------------------------------------------------ outputs that the call makes
+
+def poison(shape, dtype, copies=4):
+    """Leaves freed blocks of this size behind that hold NaN, for the allocator to hand out again."""
+    blocks = [torch.full(shape, float("nan"), dtype=dtype, device="cuda") for _ in range(copies)]
+    torch.cuda.synchronize()
+    del blocks
+
+
+def check_zeros_outside(out, off, check):
+    """Expert e's rows hold what check(e, rows) says, every other row zeros."""
+    o = off.tolist()
+    for e in range(len(o) - 1):
+        if o[e + 1] > o[e]:
+            check(e, slice(o[e], o[e + 1]))
+    assert not out[:o[0]].any() and not out[o[-1]:].any()
+
+
+MADE_CASES = [
+    # counts per expert, rows before, rows behind, N, K
+    ([0, 1], 1, 1, 33, 17),
+    ([3, 0, 4], 2, 3, 64, 48),
+    ([0, 0], 0, 40, 97, 130),          # no expert has rows
+    ([1, 2, 0, 5], 3, 2, 130, 257),
+    ([20, 0, 13], 5, 12, 96, 64),
+    ([700, 0, 300, 2], 100, 398, 131, 520),
+    ([50, 14], 0, 0, 65, 33),          # every row belongs to one
+]
+
+
+@pytest.mark.parametrize("counts,before,behind,N,K", MADE_CASES)
+def test_outputs_made_by_an_expert_call_hold_zeros_where_no_expert_has_rows(counts, before, behind, N, K):
+    E, T = len(counts), sum(counts) + before + behind
+    off = offsets_of(counts, before)
+    X, dY, w = tokens(1, T, K), tokens(2, T, N, 0.01), weight(3, E, N, K)
+    xq = q.qlora_int8_quantize_rows(X)
+    side = torch.cuda.Stream()
+    for dtype in (torch.bfloat16, torch.float32):
+        for x in (X, xq):
+            for stream in (None, side):
+                poison((T, N), dtype)
+                Y = q.qlora_int8_expert_fwd(x, w, off, out_dtype=dtype, stream=stream)
+                torch.cuda.synchronize()
+                check_zeros_outside(Y, off, lambda e, s: ref.check_forward(Y[s], fwd_ref(X[s], w, e), f"expert {e}"))
+    poison((T, K), torch.bfloat16)
+    dX = q.qlora_int8_expert_bwd(dY, w, off)
+    check_zeros_outside(dX, off, lambda e, s: ref.check_backward(dX[s], dY[s], compute_weight(w, e), f"expert {e}"))
+    assert q.qlora_device_error() == 0
+
+
+@pytest.mark.parametrize("T", [6, 40, 600])
+def test_a_graph_clears_the_rows_that_lose_their_expert(T):
+    """Outputs made inside a capture: rows that had an expert in the last replay and have none in this one are zeros."""
+    N, K = 72, 136
+    w = weight(3, 2, N, K)
+    X, dY = tokens(1, T, K), tokens(2, T, N, 0.01)
+    off = offsets_of([T // 2, T - T // 2])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Y, dX = q.qlora_int8_expert_fwd(X, w, off), q.qlora_int8_expert_bwd(dY, w, off)
+    for counts, first in (([T // 2, T - T // 2], 0), ([1, T // 3], T // 3), ([0, 0], T), ([T - 1, 0], 1)):
+        off.copy_(offsets_of(counts, first))
+        graph.replay()
+        check_zeros_outside(Y, off, lambda e, s: ref.check_forward(Y[s], fwd_ref(X[s], w, e), f"expert {e}"))
+        check_zeros_outside(dX, off,
+                            lambda e, s: ref.check_backward(dX[s], dY[s], compute_weight(w, e), f"expert {e}"))
+
+
+def test_zeroed_rows_past_32_bits():
+    T, N, K = (1 << 20) + 77, 2064, 24
+    X, w = tokens(1, T, K), weight(2, 2, N, K)
+    off = offsets_of([3, 40], T - 60)
+    poison((T, N), torch.bfloat16, copies=1)
+    Y = q.qlora_int8_expert_fwd(X, w, off)
+    check_zeros_outside(Y, off, lambda e, s: ref.check_forward(Y[s], fwd_ref(X[s], w, e), f"expert {e}"))

@@ -195,3 +195,41 @@ def test_library_status_becomes_an_exception(fake):  # noqa: F811
     with pytest.raises(q.QloraError) as e:
         q.qlora_int8_linear_fwd(bf16(5, 33), q.alloc_int8_rows((24, 33), "cpu"))
     assert e.value.status == 2
+
+
+def test_zero_rows_refusals(lib):
+    f = lib.qlora_int8_expert_zero_rows
+    assert f(P, -1, 2, 8, 1, P, None) == INVALID
+    assert f(P, 4, 0, 8, 1, P, None) == INVALID
+    assert f(P, 4, 2, 0, 1, P, None) == INVALID
+    assert f(P, 4, 2, 8, 2, P, None) == INVALID                 # unknown type
+    assert f(P, 4, 1025, 8, 1, P, None) == UNSUPPORTED
+    assert f(P, 1 << 30, 2, 8, 1, P, None) == UNSUPPORTED
+    assert f(None, 4, 2, 8, 1, P, None) == INVALID
+    assert f(P + 4, 4, 2, 8, 1, BIG, None) == INVALID
+    assert f(P, 4, 2, 8, 1, None, None) == INVALID
+    assert f(P, 4, 2, 8, 1, BIG + 2, None) == INVALID
+    assert f(P, 4, 2, 8, 1, P, None) == INVALID                 # the offsets lie in the output
+    assert f(P + 48, 4, 2, 8, 1, P, None) == INVALID
+    assert f(None, 0, 2, 8, 1, None, None) == OK
+
+
+def test_only_outputs_made_by_an_expert_call_are_cleared(fake):  # noqa: F811
+    w, we, off = q.alloc_int8_rows((24, 33), "cpu"), q.alloc_int8_rows((3, 24, 33), "cpu"), torch.zeros(4, dtype=torch.int32)
+    names = lambda: [c[0] for c in fake.calls if not c[0].endswith("_workspace_size")]  # noqa: E731
+    q.qlora_int8_expert_fwd(bf16(5, 33), we, off, out_dtype=torch.float32)
+    assert names() == ["qlora_int8_expert_zero_rows", "qlora_int8_expert_fwd"]
+    assert fake.calls[-2][1][1:5] == (5, 3, 24, 0) and fake.calls[-2][1][5] == fake.calls[-1][1][8]
+    fake.calls.clear()
+    q.qlora_int8_expert_fwd(q.alloc_int8_rows((5, 33), "cpu"), we, off)
+    assert names() == ["qlora_int8_expert_zero_rows", "qlora_int8_expert_matmul"]
+    fake.calls.clear()
+    q.qlora_int8_expert_bwd(bf16(5, 24), we, off)
+    assert names() == ["qlora_int8_expert_zero_rows", "qlora_int8_expert_bwd"]
+    assert fake.calls[-2][1][1:5] == (5, 3, 33, 1) and fake.calls[-2][1][5] == fake.calls[-1][1][8]
+    fake.calls.clear()
+    q.qlora_int8_expert_fwd(bf16(5, 33), we, off, Y=bf16(5, 24))
+    q.qlora_int8_expert_bwd(bf16(5, 24), we, off, dX=bf16(5, 33))
+    q.qlora_int8_linear_fwd(bf16(5, 33), w)
+    q.qlora_int8_linear_bwd(bf16(5, 24), w)
+    assert "qlora_int8_expert_zero_rows" not in names()
