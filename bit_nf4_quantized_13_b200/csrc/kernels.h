@@ -52,22 +52,12 @@ struct Int8Weight {
 };
 
 // The rows of each expert among T token rows: expert e has rows
-// [offsets[e], offsets[e + 1]); offsets == nullptr: one weight, all rows.
+// [offsets[e], offsets[e + 1]); offsets == nullptr: one weight, all rows.  Every
+// kernel clamps an offset to [0, T] and counts it as no less than the one before.
 struct RowRanges {
     const int32_t* offsets;
     int64_t T;
 };
-
-// Expert e's rows.  Whatever the offsets hold, the range lies in [0, T].
-__device__ __forceinline__ void expert_rows(const RowRanges& rr, int e, int* lo, int* hi) {
-    const int T = static_cast<int>(rr.T);
-    *lo = 0;
-    *hi = T;
-    if (rr.offsets) {
-        *lo = min(max(rr.offsets[e], 0), T);
-        *hi = min(max(rr.offsets[e + 1], *lo), T);
-    }
-}
 
 // int8_pair_sm100.cu -- the forward on the tensor cores, on pairs of SMs
 // (out_dtype 0: fp32, 1: bf16).  `dependent`: the launch before it on the

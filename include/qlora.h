@@ -411,8 +411,8 @@ int qlora_int8_linear_bwd(const uint16_t* dY, int64_t M, int64_t N, int64_t K, c
  * rows offsets[e] .. offsets[e + 1] - 1 use weight e (none where the two are
  * equal).  Rows before offsets[0] and from offsets[E] on belong to no expert:
  * their output rows are left as they were.  Nothing is read or written
- * outside the T rows whatever the offsets hold (each is taken clamped to
- * [0, T]; the outputs are unspecified where they are not ascending).
+ * outside the T rows whatever the offsets hold: each is taken clamped to
+ * [0, T] and as no less than the one before it.
  * 1 <= E <= QLORA_MAX_EXPERTS, else QLORA_ERR_UNSUPPORTED; T == 0 enqueues
  * nothing.
  */

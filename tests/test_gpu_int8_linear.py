@@ -610,3 +610,41 @@ def test_zeroed_rows_past_32_bits():
     poison((T, N), torch.bfloat16, copies=1)
     Y = q.qlora_int8_expert_fwd(X, w, off)
     check_zeros_outside(Y, off, lambda e, s: ref.check_forward(Y[s], fwd_ref(X[s], w, e), f"expert {e}"))
+
+
+# ------------------------------------------------------- offsets out of order
+
+def in_order(off, T):
+    """How offsets are read: clamped to [0, T], each no less than the one before it."""
+    out = [min(max(off[0], 0), T)]
+    for o in off[1:]:
+        out.append(max(out[-1], min(o, T)))
+    return out
+
+
+SCRAMBLED = [[5, 2, 8], [0, 8, 3, 8], [-5, 2, 10 ** 9], [30, 10, 50], [2 ** 31 - 1, -2 ** 31, 0], [0, 10 ** 6, 2, 10 ** 6],
+             [1, 1, 0, 2, 1, 3, 0, 2], [4 * (i % 5) - i % 7 for i in range(71)], [2 - i % 3 for i in range(1025)]]
+
+
+@pytest.mark.parametrize("off", SCRAMBLED, ids=lambda o: f"{len(o) - 1}_experts_from_{o[0]}_{o[1]}")
+@pytest.mark.parametrize("T", [1, 3, 8, 12, 50, 300])
+def test_offsets_out_of_order_mean_the_same_for_every_batch(T, off):
+    """Whichever kernel a batch of this size takes."""
+    E, N, K = len(off) - 1, 96, 64
+    w = weight(1, E, N, K)
+    X, dY = tokens(2, T, K), tokens(3, T, N, 0.01)
+    offsets, o = torch.tensor(off, dtype=torch.int32, device="cuda"), in_order(off, T)
+    full = lambda n: torch.full((T, n), 7.0, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    Y, Yq = full(N), full(N)
+    q.qlora_int8_expert_fwd(X, w, offsets, Y=Y)
+    q.qlora_int8_expert_fwd(q.qlora_int8_quantize_rows(X), w, offsets, Y=Yq)
+    dX = q.qlora_int8_expert_bwd(dY, w, offsets, dX=full(K))
+    for e in range(E):
+        s = slice(o[e], o[e + 1])
+        if o[e + 1] > o[e]:
+            ref.check_forward(Y[s], fwd_ref(X[s], w, e), f"expert {e}")
+            ref.check_backward(dX[s], dY[s], compute_weight(w, e), f"expert {e}")
+    for t in (Y, dX):
+        assert (t[:o[0]] == 7).all() and (t[o[-1]:] == 7).all()
+    assert torch.equal(Y, Yq)
+    assert q.qlora_device_error() == 0
