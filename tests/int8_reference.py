@@ -71,3 +71,41 @@ def _check(got, ref, tol, name):
         i = tuple(int(v) for v in bad.nonzero()[0])
         raise AssertionError(f"{name}: {int(bad.sum())} of {bad.numel()} off, first at {i}: "
                              f"{got[i].item()} against {ref[i].item()} (tolerance {tol[i].item():.3e})")
+
+
+def check_differences(dX, dY, W, X, elements, h=0.5):
+    """dX[m][k] for each (m, k) against a difference of the product: loss(X) =
+    sum dY (X W^T) is linear in X, so (loss(X + h e) - loss(X - h e)) / 2 h is
+    the derivative up to float64 roundings: two sums of M N terms, each a sum
+    of K, off by less than (M N + K) 2^-52 of the sum of the terms' magnitudes.
+    dX itself is off as check_backward derives, element by element."""
+    dY64, n = dY.double(), W.shape[0]
+    loss = lambda t: (dY64 * (t @ W.T)).sum().item()  # noqa: E731
+    size = (dY64.abs() * ((X.abs() + h) @ W.abs().T)).sum().item()
+    own = (dY.numel() + X.shape[1]) * 2.0 ** -52 * size / h
+    bound = dY64.abs() @ W.abs()
+    for m, k in elements:
+        e = torch.zeros_like(X)
+        e[m, k] = h
+        d = (loss(X + e) - loss(X - e)) / (2 * h)
+        tol = abs(d) * 2.0 ** -8 + bound[m, k].item() * (1.01 * n * 2.0 ** -23 * (1 + 2.0 ** -8)) + 1.01 * own
+        got = dX[m, k].item()
+        assert abs(got - d) <= tol, f"dX[{m}][{k}] = {got}, the product's difference {d} (tolerance {tol:.3e})"
+
+
+def integer_gradient(generator, M, N, K, E=None):
+    """(dY, codes, scale) of an exact gradient: dY integers up to 4, scales 1 or
+    2 by channel, so W' = code * scale is exact in bf16 and every partial sum in
+    any order is an integer below 2^24, exact in fp32 (N <= 16500)."""
+    assert N * 127 * 2 * 4 < 2 ** 24
+    lead = (N,) if E is None else (E, N)
+    kw = dict(generator=generator, device=generator.device)
+    codes = torch.randint(-127, 128, lead + (K,), dtype=torch.int8, **kw)
+    scale = torch.randint(1, 3, lead, **kw).float()
+    dY = torch.randint(-4, 5, (M, N), **kw).to(torch.bfloat16)
+    return dY, codes, scale
+
+
+def exact_gradient(dY, codes, scale):
+    """bf16 of the exact sums: integers below 2^24, so float64 and fp32 hold them."""
+    return (dY.double() @ (codes.double() * scale.double()[:, None])).float().to(torch.bfloat16)

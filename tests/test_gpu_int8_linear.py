@@ -648,3 +648,65 @@ def test_offsets_out_of_order_mean_the_same_for_every_batch(T, off):
         assert (t[:o[0]] == 7).all() and (t[o[-1]:] == 7).all()
     assert torch.equal(Y, Yq)
     assert q.qlora_device_error() == 0
+
+
+# ------------------------------------------- the gradient, element by element
+
+def test_gradient_elements_by_differences():
+    """Single elements of dX against differences of the product along their own
+    direction (a sum over all elements would hide a wrong one)."""
+    M, N, K = 40, 264, 320
+    w, dY = weight(11, N, K), tokens(12, M, N, 0.1)
+    dX = q.qlora_int8_linear_bwd(dY, w)
+    X = torch.randn((M, K), generator=gen(13), device="cuda", dtype=torch.float64)
+    picks = torch.stack([torch.randint(0, n, (120,), generator=gen(14), device="cuda") for n in (M, K)], 1).tolist()
+    ref.check_differences(dX, dY, compute_weight(w), X, picks + [[m, k] for m in (0, M - 1) for k in (0, K - 1)])
+
+
+def int8_rows(codes, scale):
+    shape = tuple(codes.shape)
+    return q.Int8Rows(torch.nn.functional.pad(codes, (0, -shape[-1] % 16)).contiguous(), scale, shape)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (16, 63, 40), (3, 65, 130), (40, 4097, 200), (100, 8192, 64),
+                                   (257, 11008, 48), (16, 11008, 512), (16, 5120, 5120), (513, 4160, 300),
+                                   (500, 10000, 128), (1, 16500, 1000), (300, 16385, 33), (600, 8200, 776),
+                                   (2049, 2304, 1024), (4700, 4100, 68)])
+def test_gradient_of_integers_is_exact(M, N, K):
+    """Every term counts, whole tiles and parts: nothing rounds before the result."""
+    dY, codes, scale = ref.integer_gradient(gen(M + N), M, N, K)
+    assert torch.equal(q.qlora_int8_linear_bwd(dY, int8_rows(codes, scale)), ref.exact_gradient(dY, codes, scale))
+    assert q.qlora_device_error() == 0
+
+
+@pytest.mark.parametrize("counts,before,behind,N,K", [([5, 0, 30], 2, 1, 5000, 130), ([300, 20], 0, 4, 4097, 64),
+                                                      ([70], 3, 5, 8192, 64), ([600, 0, 1, 511, 513], 0, 1, 4160, 776),
+                                                      ([1] * 40, 0, 0, 2049, 100), ([16, 2, 0, 33], 1, 0, 11008, 300),
+                                                      ([3900, 100, 0, 150], 1, 3, 72, 300)])
+def test_expert_gradient_of_integers_is_exact(counts, before, behind, N, K):
+    E, T = len(counts), sum(counts) + before + behind
+    off = offsets_of(counts, before)
+    dY, codes, scale = ref.integer_gradient(gen(T + N), T, N, K, E)
+    dX = torch.full((T, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    q.qlora_int8_expert_bwd(dY, int8_rows(codes, scale), off, dX=dX)
+    o = off.tolist()
+    for e in range(E):
+        s = slice(o[e], o[e + 1])
+        assert torch.equal(dX[s], ref.exact_gradient(dY[s], codes[e], scale[e])), f"expert {e}"
+    assert (dX[:o[0]] == 7).all() and (dX[o[-1]:] == 7).all()
+
+
+@pytest.mark.parametrize("N,K", [(65, 300), (264, 5120), (4097, 200), (8192, 64), (11008, 48)])
+def test_gradient_of_one_channel_is_its_weight(N, K):
+    """dY = one 1 a row: dX is that channel's W' = bf16(RN32(code * scale)),
+    rounded and not truncated, bit for bit.  All channels at once, and a few
+    rows whose tiles are cut along the contraction."""
+    w = weight(N + K, N, K)
+    W = compute_weight(w).to(torch.bfloat16)
+    assert torch.equal(q.qlora_int8_linear_bwd(torch.eye(N, dtype=torch.bfloat16, device="cuda"), w), W)
+    edges = [n for b in range(64, N, 64) for n in (b - 1, b)] + [0, N - 1]
+    for first in range(0, len(edges), 100):
+        at = torch.tensor(edges[first:first + 100], device="cuda")
+        dY = torch.zeros((len(at), N), dtype=torch.bfloat16, device="cuda")
+        dY[torch.arange(len(at), device="cuda"), at] = 1
+        assert torch.equal(q.qlora_int8_linear_bwd(dY, w), W[at])

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import bit_nf4_quantized_13_b200 as q
+import int8_reference as ref
 from test_binding_cpu import fake  # noqa: F401  (the recorder fixture)
 
 OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
@@ -233,3 +234,56 @@ def test_only_outputs_made_by_an_expert_call_are_cleared(fake):  # noqa: F811
     q.qlora_int8_linear_fwd(bf16(5, 33), w)
     q.qlora_int8_linear_bwd(bf16(5, 24), w)
     assert "qlora_int8_expert_zero_rows" not in names()
+
+
+# The gradient tests' own checks, fed with right and with wrong gradients.
+
+def small_gradient():
+    g = torch.Generator()
+    g.manual_seed(5)
+    M, N, K = 40, 264, 320
+    codes, scale, _ = ref.quantize_rows(torch.randn((N, K), generator=g) * 0.02)
+    W = ref.compute_weight(codes, scale)
+    dY = (torch.randn((M, N), generator=g) * 0.1).to(torch.bfloat16)
+    X = torch.randn((M, K), generator=g, dtype=torch.float64)
+    picks = torch.stack([torch.randint(0, n, (120,), generator=g) for n in (M, K)], 1).tolist()
+    return dY, codes, scale, W, X, picks + [[m, k] for m in (0, M - 1) for k in (0, K - 1)]
+
+
+def bf16_product(dY, W):
+    return (dY.float() @ W.float()).to(torch.bfloat16)
+
+
+def test_the_difference_check_rejects_wrong_gradients():
+    dY, codes, scale, W, X, picks = small_gradient()
+    good = bf16_product(dY, W)
+    ref.check_differences(good, dY, W, X, picks)
+    zero_row, zero_column = good.clone(), good.clone()
+    zero_row[picks[0][0]], zero_column[:, picks[1][1]] = 0, 0
+    wrong = {"scaled by 0.99": (bf16_product(dY, W).float() * 0.99).to(torch.bfloat16), "a row of zeros": zero_row,
+             "a column of zeros": zero_column, "the last term dropped": bf16_product(dY[:, :-1], W[:-1]),
+             "a token's neighbour": good.roll(1, 0), "a column's neighbour": good.roll(1, 1),
+             "the scales dropped": bf16_product(dY, codes)}
+    for name, dX in wrong.items():
+        with pytest.raises(AssertionError):
+            ref.check_differences(dX, dY, W, X, picks)
+            pytest.fail(f"accepted: {name}")
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 11008, 48), (5, 4097, 70), (3, 16500, 20)])
+def test_the_exact_checks_reject_wrong_gradients(M, N, K):
+    g = torch.Generator()
+    g.manual_seed(N)
+    dY, codes, scale = ref.integer_gradient(g, M, N, K)
+    W = codes.double() * scale.double()[:, None]
+    want = ref.exact_gradient(dY, codes, scale)
+    assert torch.equal(bf16_product(dY, W), want)  # fp32 sums in torch's order: exact too
+    assert (dY.double().abs() @ W.abs()).max() < 2 ** 24
+    for lost in (0, 63, 64, N // 2, N - 1):
+        part = dY.clone()
+        part[:, lost] = 0
+        assert dY[:, lost].any() and not torch.equal(bf16_product(part, W), want), lost
+    codes, scale, _ = ref.quantize_rows(torch.randn((300, K), generator=g) * 0.02)
+    held = ref.round32(codes * scale[:, None]).float()
+    cut = (held.view(torch.int32) & -65536).view(torch.float32)  # W' truncated to bf16
+    assert not torch.equal(cut.to(torch.bfloat16), ref.compute_weight(codes, scale).to(torch.bfloat16))
