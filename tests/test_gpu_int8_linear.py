@@ -710,3 +710,59 @@ def test_gradient_of_one_channel_is_its_weight(N, K):
         dY = torch.zeros((len(at), N), dtype=torch.bfloat16, device="cuda")
         dY[torch.arange(len(at), device="cuda"), at] = 1
         assert torch.equal(q.qlora_int8_linear_bwd(dY, w), W[at])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(9, 9217, 130), (12, 9472, 1111), (16, 13824, 5120), (13, 20001, 64), (16, 9216, 300)])
+def test_linear_fwd_of_a_decode_batch_over_a_wide_weight(M, N, K, dtype):
+    """9 to 16 tokens on both sides of the width from which the tensor-core
+    kernel's tiles fill half of the SM pairs (more than 36 tiles of 256 channels)."""
+    X, w = tokens(M + N, M, K), weight(K, N, K)
+    Y = q.qlora_int8_linear_fwd(X, w, out_dtype=dtype)
+    ref.check_forward(Y, fwd_ref(X, w), "Y")
+    assert torch.equal(q.qlora_int8_linear_fwd(q.qlora_int8_quantize_rows(X), w, out_dtype=dtype), Y)
+    assert q.qlora_device_error() == 0
+
+
+@pytest.mark.parametrize("counts,before,behind,N,K", [([70], 3, 5, 64, 11008), ([300], 0, 212, 130, 9000), ([1], 511, 0, 512, 4096),
+                                                      ([0], 9, 0, 64, 11008), ([2], 3, 1, 700, 4096)])
+def test_one_expert_that_has_some_of_the_rows(counts, before, behind, N, K):
+    """What the host cuts for all T rows, the device cuts for the expert's."""
+    T, off = sum(counts) + before + behind, offsets_of(counts, before)
+    s = slice(before, before + counts[0])
+    X, dY, w = tokens(T, T, K), tokens(T + 1, T, N, 0.01), weight(K, 1, N, K)
+    Y, dX = q.qlora_int8_expert_fwd(X, w, off), q.qlora_int8_expert_bwd(dY, w, off)
+    check_zeros_outside(Y, off, lambda e, s: ref.check_forward(Y[s], fwd_ref(X[s], w, e)))
+    check_zeros_outside(dX, off, lambda e, s: ref.check_backward(dX[s], dY[s], compute_weight(w, e)))
+    dense = q.Int8Rows(w.codes[0], w.scale[0], (N, K))
+    if counts[0]:
+        assert torch.equal(Y[s], q.qlora_int8_linear_fwd(X[s].clone(), dense))
+    assert q.qlora_device_error() == 0
+
+
+# --------------------------------------------------- the binding on the device
+
+def test_calls_go_to_the_current_stream():
+    """The raw handle that the binding passes is the current stream's."""
+    assert q._stream() == torch.cuda.current_stream().cuda_stream
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert q._stream() == side.cuda_stream
+    assert q._stream(side) == side.cuda_stream
+    assert q._stream() == torch.cuda.current_stream().cuda_stream != side.cuda_stream
+
+
+def test_tensors_of_the_host_or_with_strides_are_refused():
+    w, X = weight(1, 24, 32), tokens(2, 8, 32)
+    off = offsets_of([4, 4])
+    for call in (lambda: q.qlora_int8_linear_fwd(X.cpu(), w),
+                 lambda: q.qlora_int8_linear_fwd(tokens(2, 32, 8).t(), w),
+                 lambda: q.qlora_int8_linear_fwd(X, q.Int8Rows(w.codes.cpu(), w.scale, w.shape)),
+                 lambda: q.qlora_int8_linear_fwd(X, w, Y=torch.zeros((8, 48), dtype=torch.bfloat16, device="cuda")[:, ::2]),
+                 lambda: q.qlora_int8_expert_fwd(X, weight(3, 2, 24, 32), off.cpu()),
+                 lambda: q.qlora_int8_expert_bwd(tokens(2, 8, 24).cpu(), weight(3, 2, 24, 32), off),
+                 lambda: q.qlora_int8_quantize_rows(X.t())):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(q.QloraError):
+        q.qlora_int8_linear_fwd(tokens(2, 9, 8 * 32 + 1).flatten()[1:8 * 32 + 1].view(8, 32), w)  # not 16-byte aligned
