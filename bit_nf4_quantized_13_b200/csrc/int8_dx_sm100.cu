@@ -12,7 +12,7 @@
 // The conversion of the weights is the other half of the work, and of a tile
 // of few tokens nearly all of it: 64 x 128 codes per CTA for 4 MMAs.  Its warps
 // do nothing else (when they also loaded the codes through registers and wrote
-// the outputs, a stage of few tokens took 700 to 900 cycles instead of 475):
+// the outputs, a stage of few tokens took 700 to 900 cycles):
 //
 //   warp 0       copies dY's token halves (TMA, bytes on the even CTA's barrier)
 //   warp 1       issues the MMAs (one thread of the even CTA)
@@ -23,17 +23,19 @@
 //   warps 20-23  epilogue of the TMEM lane quarter w % 4, under the next tile's
 //                stages (two accumulators)
 //
-// A stage takes 500 to 570 cycles with few tokens and 680 to 750 with 256, where
-// its MMAs take 156 and 512: 4096 x 11008 x 4096 takes 241 us (tensor pipe 86%
-// active), 1500 rows over 64 experts of 1024 x 2048 48 us (137 MB, 22 us at the
-// copy rate).  Cycle counters: of a converter warp's 2450 a turn (one stage in
-// four) loading and converting takes 800, storing and the proxy fence 550,
-// waiting for the slot 600; the shared memory's 88 KiB a stage alone are 690 cycles at 256
-// tokens.  Without the arithmetic 706 of 752 remain.  Tried and slower: the
+// A stage takes 530 to 590 cycles with up to 128 tokens and 670 with 160 to 256
+// (74 tiles, by the contraction's length), where its MMAs take 156 at 32 and 512
+// at 256: 4096 x 11008 x 4096 takes 238 us (tensor pipe 86% active), 1500 rows
+// over 64 experts of 1024 x 2048 47 us (137 MB, 22 us at the copy rate).  Cycle
+// counters in a large product (752 a stage): of a converter warp's 2450 a turn
+// (one stage in four) loading and converting takes 800, storing and the proxy
+// fence 550, waiting for the slot 600.  The shared memory's traffic (codes and
+// bf16 tile in and out, dY in and out: 80 KiB a stage of 256 tokens) is 640 cycles
+// at 128 bytes each.  Without the arithmetic 706 of 752 remain.  Tried and slower: the
 // weights through tensor memory (no shared-memory operand, but 500 to 600 cycles
 // a stage of 128 to 192 tokens), tiles of 512 tokens with codes loaded through
 // registers, polling by one lane of a warp (+20%).  One barrier a stage for both
-// operands saves the issuing thread a wait (1500 rows: 52 -> 49 us).
+// operands saves the issuing thread a wait (1500 rows: 3 us of 52).
 //
 // Conversion: a code, offset by 128, is placed in the mantissa of 2^23 by a
 // byte permute; one subtraction gives the exact value, one multiplication
@@ -443,8 +445,8 @@ int max_pairs() {
     return n;
 }
 
-// 256 x 5120 x 5120 takes 41 us in whole tiles and 30 in three parts, 500 x
-// 10000 x 128 72 and 30.
+// In a captured graph 256 x 5120 x 5120 takes 34.5 us in whole tiles and 23.6 in
+// three parts, 500 x 10000 x 128 54 and 25, 16 x 5120 x 5120 26 and 18.
 Schedule schedule(const RowRanges& rr, const Int8Weight& w) {
     return schedule_of(rr, w.E, w.K, ceil_div(w.N, kBK), kTileTok, 32, sm_pairs());
 }

@@ -310,8 +310,8 @@ cudaError_t gemv_any(const GemvParams& p, int out_dtype, cudaStream_t st, bool d
 }  // namespace
 
 // Up to 8 tokens always.  Up to 16, unless the tensor-core kernel's tiles (256
-// channels each) fill half of the SM pairs: 16 x 13824 x 5120 takes 24.6 us
-// here and 20.5 there, 16 x 4096 x 4096 12.3 and 16.4.
+// channels each) fill half of the SM pairs: in a captured graph 16 x 13824 x 5120
+// takes 19.6 us here and 17.1 there, 16 x 4096 x 4096 7.2 and 11.3.
 bool int8_gemv_pays(int64_t T, const Int8Weight& w) {
     if (T <= 8) return true;
     return T <= kMaxTokens && int8_tiles(T, w.E, w.N, 256) * 4 < num_sms();

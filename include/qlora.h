@@ -377,7 +377,9 @@ int qlora_int8_quantize_rows(const void* x, int x_dtype, int64_t rows, int64_t K
  * as written by qlora_int8_quantize_rows:
  *   Y[m][n] = out(RN32(RN32(RN32(sum_k x_codes[m][k] w_codes[n][k]) * x_scale[m]) * w_scale[n]))
  * The sum is exact (32-bit integers); out is fp32 (out_dtype 0) or bf16 bits
- * (out_dtype 1).  Y: M x N.
+ * (out_dtype 1).  Y: M x N.  The product with x_scale, taken first, may exceed
+ * fp32 (Y infinite, whatever w_scale is) for tokens whose largest |x| is above
+ * FLT_MAX / (127 K); below that it loses nothing.
  */
 size_t qlora_int8_matmul_workspace_size(int64_t M, int64_t N, int64_t K);
 int qlora_int8_matmul(const int8_t* x_codes, const float* x_scale, int64_t M, int64_t N, int64_t K,

@@ -766,3 +766,23 @@ def test_tensors_of_the_host_or_with_strides_are_refused():
             call()
     with pytest.raises(q.QloraError):
         q.qlora_int8_linear_fwd(tokens(2, 9, 8 * 32 + 1).flatten()[1:8 * 32 + 1].view(8, 32), w)  # not 16-byte aligned
+
+
+@pytest.mark.parametrize("M", [2, 12, 300])
+@pytest.mark.parametrize("K", [320, 8192])
+def test_the_scales_are_taken_in_their_order(M, K):
+    """Y = RN32(RN32(RN32(sum) x_scale) w_scale) to the bit, at either end of
+    fp32: for tokens above FLT_MAX / (127 K) the first product may be infinite."""
+    w = q.qlora_int8_quantize_rows(torch.randn((70, K), generator=gen(2), device="cuda") * 1e-3)
+    for size in (1.0, 1e-37, 1e-34, 3e32, 1e35, 1e38):
+        x = torch.rand((M, K), generator=gen(M), device="cuda") + 1
+        x[1::2] *= -1
+        X = (x * size).to(torch.bfloat16)
+        xq = q.qlora_int8_quantize_rows(X)
+        sums = (xq.codes.double() @ w.codes.double().T).float()  # below 2^53, rounded once
+        want = (sums * xq.scale[:, None]) * w.scale
+        Y = q.qlora_int8_linear_fwd(X, w, out_dtype=torch.float32)
+        assert torch.equal(Y, want) and torch.equal(q.qlora_int8_linear_fwd(xq, w, out_dtype=torch.float32), want)
+        assert torch.equal(q.qlora_int8_linear_fwd(X, w), want.to(torch.bfloat16))
+        top = X.double().abs().max().item()
+        assert want.isfinite().all() or top > ref.FLT_MAX / (127 * K)
